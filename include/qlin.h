@@ -3,9 +3,11 @@
  *
  *     y[M,N] = dequant(W[N,K]) . x[M,K],   M = 1..16 tokens
  *
- * in four variants: W8A8 INT8, FP8-E4M3 weight-only (and FP8 W8A8 with
- * E4M3 / E5M2 codes), 128x128 block-scaled FP8 with UE8M0 scales, and the
- * MXFP4 expert GEMV behind top-k routing (also as a routed expert FFN).
+ * in five variants: W8A8 INT8, FP8-E4M3 weight-only (and FP8 W8A8 with
+ * E4M3 / E5M2 codes), 128x128 block-scaled FP8 with UE8M0 scales, the
+ * MXFP4 expert GEMV behind top-k routing (also as a routed expert FFN), and
+ * 4-bit weights with group scales (also as a gated feed-forward front, and
+ * both with their input gradients).
  *
  * Sources (web pages, by title and section):
  *   [Z100] "Hygon Z100 (gfx906) vLLM adaptation: optimisation and operator
@@ -39,7 +41,8 @@
  * - M (tokens): the dense entry points (INT8, FP8, FP8 W8A8, block FP8 and
  *   their quantisers) and qlin_moe_mxfp4 accept 1 <= M <= QLIN_MAX_M_PREFILL;
  *   up to 16 they run the decode kernels, above 16 a tiled (grouped, for
- *   the MoE) matrix-core GEMM with the same arithmetic contract.  The routed
+ *   the MoE) matrix-core GEMM with the same arithmetic contract.  The 4-bit
+ *   weight calls accept the same range.  The routed
  *   expert FFN and the per-tensor FP8 quantiser take 1 <= M <= QLIN_MAX_M.
  * - Base pointers and row pitches of weights, codes and bf16 activations must
  *   be 16-byte aligned (128-bit loads); scale arrays must be naturally
@@ -354,6 +357,82 @@ int qlin_moe_ffn_mxfp4(const void* x, int64_t ldx, int64_t M, int64_t H,
                        int32_t* topk_ids, float* topk_w,
                        void* y, int64_t ldy,
                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * (f) 4-bit weights with group scales: linear layer, gated feed-forward
+ *     front, and the input gradients of both
+ * ------------------------------------------------------------------------
+ * The weight matrix of these calls, N rows of K (group G, g = k / G):
+ *   W[n,k] = ws[n,g] * (code[n,k] - zero[n,g])
+ *   w   uint8 [N, ldw]   codes 0..15, element 2i in the LOW nibble of byte i;
+ *                        pitch ldw in bytes, ldw >= K/2, ldw % 16 == 0
+ *   ws  16-bit [N, K/G]  scales in the activations' type (row-major, dense)
+ *   wz  uint8 [N, K/G]   zero points 0..15, or NULL: 8 everywhere
+ * dtype is the type of every 16-bit operand and result of the call.
+ * Requires K % 32 == 0, 32 <= K <= 2^20, G >= 32, G % 32 == 0, K % G == 0,
+ * 1 <= N <= 2^20, 1 <= M <= QLIN_MAX_M_PREFILL.  All sums are fp32.  The
+ * weights are frozen: there is no gradient of codes, scales or zero points. */
+enum {
+    QLIN_DT_BF16 = 0,
+    QLIN_DT_FP16 = 1
+};
+enum {
+    QLIN_ACT_SILU = 0,      /* act(g) = g / (1 + e^-g) */
+    QLIN_ACT_GELU_TANH = 1  /* act(g) = g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
+};
+
+/* y[m,n] = r16( sum_k x[m,k] * W[n,k] + bias[n] ), one rounding.
+ *   x 16-bit [M, ldx] (16-byte aligned, ldx % 8 == 0); bias 16-bit [N] or
+ *   NULL; y 16-bit [M, ldy].
+ * A weight is rounded once to dtype before it is multiplied. */
+int qlin_gemv_w4(const void* x, int64_t ldx, int64_t M, int64_t K, int dtype,
+                 const uint8_t* w, int64_t ldw, int64_t N, const void* ws, const uint8_t* wz, int64_t group,
+                 const void* bias, void* y, int64_t ldy, void* stream);
+
+/* Bytes of device workspace qlin_gemv_w4_bwd needs for N rows of K: fp32
+ * partial sums where the reduction over N is split to fill the chip, 0
+ * elsewhere (and for sizes the call refuses). */
+size_t qlin_gemv_w4_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* The input gradient dx[m,k] = r16( sum_n dy[m,n] * W[n,k] ).
+ *   dy 16-bit [M, lddy]: 16-byte aligned, lddy >= N, lddy % 8 == 0; every
+ *      row is read up to the next multiple of 8 elements after N (what it
+ *      holds there does not matter, but it must be readable);
+ *   dx 16-bit [M, lddx], must not overlap dy;
+ *   workspace: 16-byte aligned, at least qlin_gemv_w4_bwd_workspace_bytes()
+ *      (NULL where that is 0); its contents on entry do not matter; calls
+ *      that can overlap need one each.
+ * A weight is rounded once to dtype before it is multiplied.  The result
+ * does not depend on timing (no atomics; partial sums are added in order). */
+int qlin_gemv_w4_bwd(const void* dy, int64_t lddy, int64_t M, int64_t N, int dtype,
+                     const uint8_t* w, int64_t ldw, int64_t K, const void* ws, const uint8_t* wz, int64_t group,
+                     void* dx, int64_t lddx, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gated feed-forward front, both projections, the activation and the product
+ * in one kernel.  w13 has 2I rows: gate rows 0..I-1, then up rows I..2I-1.
+ *   g[m,i] = sum_k x[m,k] W[i,k],  u[m,i] = sum_k x[m,k] W[I+i,k]   (fp32)
+ *   y[m,i] = r16( act(g) * u )                                [M, ldy]
+ *   gu (optional) 16-bit [M, ldgu >= 2I]: r16(g) in columns 0..I-1, r16(u)
+ *   in columns I..2I-1, for qlin_glu_w4_bwd.  The down projection is
+ *   qlin_gemv_w4 on y. */
+int qlin_glu_w4(const void* x, int64_t ldx, int64_t M, int64_t K, int dtype,
+                const uint8_t* w13, int64_t ldw, int64_t I, const void* s13, const uint8_t* z13, int64_t group,
+                int act, void* y, int64_t ldy, void* gu, int64_t ldgu, void* stream);
+
+/* Backward of qlin_glu_w4.
+ *   dgu[m,:] = r16( [ dy u act'(g), dy act(g) ] )        16-bit [M, lddgu]
+ *   dx[m,k]  = r16( sum_{j < 2I} dgu[m,j] * W[j,k] )     16-bit [M, lddx]
+ * g and u come from gu if it is given (x is then unused and may be NULL), and
+ * are otherwise recomputed from x in fp32 by the forward kernel.  dgu (the
+ * gradient of [g, u], which adapters on the projections need) is always
+ * written: 16-byte aligned, lddgu >= 2I, lddgu % 8 == 0, every row readable
+ * up to the next multiple of 8 after 2I; it may be gu itself.  dx may be NULL
+ * (not computed).  workspace as in qlin_gemv_w4_bwd with N = 2I. */
+int qlin_glu_w4_bwd(const void* dy, int64_t lddy, int64_t M, int64_t I, int dtype, int act,
+                    const void* x, int64_t ldx, const void* gu, int64_t ldgu,
+                    const uint8_t* w13, int64_t ldw, int64_t K, const void* s13, const uint8_t* z13, int64_t group,
+                    void* dgu, int64_t lddgu, void* dx, int64_t lddx,
+                    void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -13,14 +13,19 @@ torch.uint8 (a torch.float8_e4m3fn tensor may be passed for E4M3 codes).
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
-from ._lib import QLIN_FMT_E4M3, QLIN_FMT_E5M2, QlinError, check, load, status_str  # noqa: F401
+from ._lib import (QLIN_ACT_GELU_TANH, QLIN_ACT_SILU, QLIN_DT_BF16, QLIN_DT_FP16, QLIN_FMT_E4M3,  # noqa: F401
+                   QLIN_FMT_E5M2, QlinError, check, load, status_str)
 
 __all__ = [
     "QlinError", "qlin_act_quant_i8", "qlin_gemv_i8", "qlin_linear_i8", "qlin_gemv_fp8", "qlin_gemv_fp8_blk",
     "qlin_act_quant_fp8", "qlin_gemv_fp8_w8a8", "QLIN_FMT_E4M3", "QLIN_FMT_E5M2", "qlin_gemv_fp8_blk_ex",
     "qlin_moe_mxfp4", "qlin_moe_mxfp4_workspace_bytes", "qlin_moe_mxfp4_noalloc", "status_str",
+    "qlin_gemv_w4", "qlin_gemv_w4_bwd", "qlin_gemv_w4_bwd_workspace_bytes", "qlin_glu_w4", "qlin_glu_w4_bwd",
+    "QLIN_DT_BF16", "QLIN_DT_FP16", "QLIN_ACT_SILU", "QLIN_ACT_GELU_TANH",
 ]
 
 
@@ -28,6 +33,15 @@ def _stream(t: torch.Tensor, stream):
     if stream is None:
         return torch.cuda.current_stream(t.device).cuda_stream
     return getattr(stream, "cuda_stream", stream)
+
+
+_NO_SWITCH = contextlib.nullcontext()
+
+
+def _on(t: torch.Tensor):
+    """The device of `t` made current (kernels are launched on the current device)."""
+    d = t.device
+    return _NO_SWITCH if d.index is None or d.index == torch.cuda.current_device() else torch.cuda.device(d)
 
 
 def _need(t: torch.Tensor, name: str, dtypes, dims: int):
@@ -370,3 +384,152 @@ def qlin_moe_ffn_mxfp4(x, wr, w13, s13, w2, s2, topk, alpha=1.0, limit=10.0, y=N
     logits = workspace[:M * E * 4].view(torch.float32).view(M, E)
     act = workspace[o_act:o_act + M * topk * I * 2].view(torch.bfloat16).view(M * topk, I)
     return y, ids, gw, logits, act
+
+
+_DT16 = {torch.bfloat16: QLIN_DT_BF16, torch.float16: QLIN_DT_FP16}
+
+
+def _w4_weight(a, name, w, ws, wz):
+    """Checks a 4-bit weight against the 16-bit operand `a`; returns (N, K, group, dtype flag)."""
+    dt = _DT16.get(a.dtype)
+    if dt is None:
+        raise TypeError(f"{name}: dtype {a.dtype} not in {tuple(_DT16)}")
+    _need(a, name, (a.dtype,), 2)
+    _need(w, "w", (torch.uint8,), 2)
+    _need(ws, "ws", (a.dtype,), 2)
+    N, Kh = w.shape
+    K, groups = 2 * Kh, ws.shape[1]
+    if ws.shape[0] != N or groups < 1 or K % groups or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous [{N}, K / group], got {tuple(ws.shape)}")
+    if wz is not None:
+        _need(wz, "wz", (torch.uint8,), 2)
+        if wz.shape != ws.shape or not wz.is_contiguous():
+            raise ValueError(f"wz must be contiguous {tuple(ws.shape)}, got {tuple(wz.shape)}")
+    for t in (w, ws, wz):
+        if t is not None and t.device != a.device:
+            raise ValueError(f"weights on {t.device}, {name} on {a.device}")
+    return N, K, K // groups, dt
+
+
+def _out16(t, name, like, rows, cols):
+    """An output of `like`'s type and device: allocated, or checked."""
+    if t is None:
+        return torch.empty((rows, cols), dtype=like.dtype, device=like.device)
+    _need(t, name, (like.dtype,), 2)
+    if tuple(t.shape) != (rows, cols) or t.device != like.device:
+        raise ValueError(f"{name} must be [{rows}, {cols}] on {like.device}, got {tuple(t.shape)} on {t.device}")
+    return t
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _pitch(t):
+    """Row pitch in elements (a single row has no pitch of its own)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _pitch8(t):
+    """_pitch rounded up to 8 elements for a single row, whose stride may be anything."""
+    return t.stride(0) if t.shape[0] > 1 else (max(t.stride(0), t.shape[1]) + 7) // 8 * 8
+
+
+def qlin_gemv_w4(x, w, ws, wz=None, bias=None, y=None, stream=None):
+    """Linear layer on 4-bit weights with group scales: x bf16 or fp16 [M, K]; w
+    uint8 [N, K/2] (element 2i in the low nibble, any row pitch that is a
+    multiple of 16); ws [N, K/group] of x's dtype; wz uint8 [N, K/group] or None
+    (zero point 8); bias [N] of x's dtype or None.  Returns y [M, N]."""
+    N, K, group, dt = _w4_weight(x, "x", w, ws, wz)
+    M = x.shape[0]
+    if x.shape[1] != K:
+        raise ValueError(f"w has K={K}, x has K={x.shape[1]}")
+    if bias is not None:
+        _need(bias, "bias", (x.dtype,), 1)
+        if bias.shape[0] != N or bias.device != x.device:
+            raise ValueError(f"bias must be [{N}] on {x.device}")
+    y = _out16(y, "y", x, M, N)
+    with _on(x):
+        check(load().qlin_gemv_w4(x.data_ptr(), _pitch8(x), M, K, dt, w.data_ptr(), w.stride(0), N, ws.data_ptr(),
+                                  _ptr(wz), group, _ptr(bias), y.data_ptr(), _pitch(y), _stream(x, stream)),
+              "qlin_gemv_w4")
+    return y
+
+
+def qlin_gemv_w4_bwd_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(load().qlin_gemv_w4_bwd_workspace_bytes(M, N, K))
+
+
+def _w4_workspace(workspace, M, N, K, like):
+    need = qlin_gemv_w4_bwd_workspace_bytes(M, N, K)
+    if workspace is None and need:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=like.device)
+    return (None, 0) if workspace is None else (workspace, workspace.numel() * workspace.element_size())
+
+
+def qlin_gemv_w4_bwd(dy, w, ws, wz=None, dx=None, workspace=None, stream=None):
+    """Input gradient of qlin_gemv_w4: dy [M, N] (row pitch a multiple of 8) and
+    the weight -> dx [M, K]."""
+    N, K, group, dt = _w4_weight(dy, "dy", w, ws, wz)
+    M = dy.shape[0]
+    if dy.shape[1] != N:
+        raise ValueError(f"w has N={N}, dy has N={dy.shape[1]}")
+    dx = _out16(dx, "dx", dy, M, K)
+    ws_buf, ws_bytes = _w4_workspace(workspace, M, N, K, dy)
+    with _on(dy):
+        check(load().qlin_gemv_w4_bwd(dy.data_ptr(), _pitch8(dy), M, N, dt, w.data_ptr(), w.stride(0), K,
+                                      ws.data_ptr(), _ptr(wz), group, dx.data_ptr(), _pitch(dx), _ptr(ws_buf),
+                                      ws_bytes, _stream(dy, stream)), "qlin_gemv_w4_bwd")
+    return dx
+
+
+def qlin_glu_w4(x, w13, s13, z13=None, act=QLIN_ACT_SILU, y=None, gu=None, stream=None):
+    """Gated feed-forward front on 4-bit weights: w13 uint8 [2I, K/2] (gate rows,
+    then up rows), s13 / z13 as ws / wz of qlin_gemv_w4.  Returns
+    y = act(x Wg^T) * (x Wu^T) [M, I]; gu [M, 2I], if given, receives gate and up."""
+    N, K, group, dt = _w4_weight(x, "x", w13, s13, z13)
+    M, I = x.shape[0], N // 2
+    if x.shape[1] != K or N != 2 * I:
+        raise ValueError(f"w13 is [{N}, {K}], x has K={x.shape[1]}: rows must be 2I, K equal")
+    y = _out16(y, "y", x, M, I)
+    if gu is not None:
+        _out16(gu, "gu", x, M, N)
+    with _on(x):
+        check(load().qlin_glu_w4(x.data_ptr(), _pitch8(x), M, K, dt, w13.data_ptr(), w13.stride(0), I, s13.data_ptr(),
+                                 _ptr(z13), group, int(act), y.data_ptr(), _pitch(y), _ptr(gu),
+                                 0 if gu is None else _pitch(gu), _stream(x, stream)), "qlin_glu_w4")
+    return y
+
+
+def qlin_glu_w4_bwd(dy, w13, s13, z13=None, act=QLIN_ACT_SILU, x=None, gu=None, dgu=None, dx=None, workspace=None,
+                    need_dx=True, stream=None):
+    """Backward of qlin_glu_w4 from dy [M, I] and either the kept gu [M, 2I] or x
+    [M, K] (gate and up are then recomputed).  Returns (dx [M, K], dgu [M, 2I]);
+    need_dx=False skips the input gradient and returns (None, dgu)."""
+    N, K, group, dt = _w4_weight(dy, "dy", w13, s13, z13)
+    M, I = dy.shape[0], N // 2
+    if dy.shape[1] * 2 != N:
+        raise ValueError(f"w13 has {N} rows, dy has I={dy.shape[1]}")
+    if x is None and gu is None:
+        raise ValueError("either x or gu is needed")
+    if x is not None:
+        _out16(x, "x", dy, M, K)
+    if gu is not None:
+        _out16(gu, "gu", dy, M, N)
+    if dgu is None:  # row pitch a multiple of 8, as the second product reads it
+        dgu = torch.empty((M, (N + 7) // 8 * 8), dtype=dy.dtype, device=dy.device)[:, :N]
+    else:
+        _out16(dgu, "dgu", dy, M, N)
+    ws_buf, ws_bytes = None, 0
+    if need_dx:
+        dx = _out16(dx, "dx", dy, M, K)
+        ws_buf, ws_bytes = _w4_workspace(workspace, M, N, K, dy)
+    else:
+        dx = None
+    with _on(dy):
+        check(load().qlin_glu_w4_bwd(dy.data_ptr(), _pitch(dy), M, I, dt, int(act), _ptr(x),
+                                     0 if x is None else _pitch8(x), _ptr(gu), 0 if gu is None else _pitch(gu),
+                                     w13.data_ptr(), w13.stride(0), K, s13.data_ptr(), _ptr(z13), group,
+                                     dgu.data_ptr(), _pitch8(dgu), _ptr(dx), 0 if dx is None else _pitch(dx),
+                                     _ptr(ws_buf), ws_bytes, _stream(dy, stream)), "qlin_glu_w4_bwd")
+    return dx, dgu

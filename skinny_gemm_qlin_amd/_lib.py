@@ -26,10 +26,17 @@ EXPORTS = (
     "qlin_gemv_fp8_blk", "qlin_moe_mxfp4_workspace_bytes", "qlin_moe_mxfp4",
     "qlin_moe_ffn_mxfp4_workspace_bytes", "qlin_moe_ffn_mxfp4", "qlin_act_quant_fp8", "qlin_gemv_fp8_w8a8",
     "qlin_gemv_fp8_blk_ex", "qlin_moe_mxfp4_noalloc", "qlin_linear_i8",
+    "qlin_gemv_w4", "qlin_gemv_w4_bwd_workspace_bytes", "qlin_gemv_w4_bwd", "qlin_glu_w4", "qlin_glu_w4_bwd",
 )
 
 QLIN_FMT_E4M3 = 0
 QLIN_FMT_E5M2 = 1
+
+QLIN_DT_BF16 = 0
+QLIN_DT_FP16 = 1
+
+QLIN_ACT_SILU = 0
+QLIN_ACT_GELU_TANH = 1
 
 
 class QlinError(RuntimeError):
@@ -81,6 +88,17 @@ def load() -> ctypes.CDLL:
     lib.qlin_moe_ffn_mxfp4.argtypes = [P, I64, I64, I64, P, I64, I64, P, P, I64, P, P, F, F, P, P, P, I64,
                                        P, SZ, P]
     lib.qlin_moe_ffn_mxfp4.restype = I
+    lib.qlin_gemv_w4.argtypes = [P, I64, I64, I64, I, P, I64, I64, P, P, I64, P, P, I64, P]
+    lib.qlin_gemv_w4.restype = I
+    lib.qlin_gemv_w4_bwd_workspace_bytes.argtypes = [I64, I64, I64]
+    lib.qlin_gemv_w4_bwd_workspace_bytes.restype = SZ
+    lib.qlin_gemv_w4_bwd.argtypes = [P, I64, I64, I64, I, P, I64, I64, P, P, I64, P, I64, P, SZ, P]
+    lib.qlin_gemv_w4_bwd.restype = I
+    lib.qlin_glu_w4.argtypes = [P, I64, I64, I64, I, P, I64, I64, P, P, I64, I, P, I64, P, I64, P]
+    lib.qlin_glu_w4.restype = I
+    lib.qlin_glu_w4_bwd.argtypes = [P, I64, I64, I64, I, I, P, I64, P, I64, P, I64, I64, P, P, I64, P, I64, P, I64,
+                                    P, SZ, P]
+    lib.qlin_glu_w4_bwd.restype = I
     _lib = lib
     return lib
 

@@ -1,0 +1,97 @@
+// w4_gemm.hip -- launchers of the 4-bit weight GEMM (w4_gemm.hpp).
+#include "w4_gemm.hpp"
+
+namespace qlin {
+
+namespace {
+
+template <int T, bool BWD, int EPI, int BM, int BN, int WGM, int WGN>
+hipError_t run(W4GemmParams p, int64_t splits, hipStream_t st) {
+    constexpr int CT = EPI == kW4Glu || EPI == kW4GluBwd ? BN / 2 : BN;
+    const int64_t tiles = ((p.M + BM - 1) / BM) * ((p.C + CT - 1) / CT);
+    const int64_t nsteps = (p.R + 63) / 64;
+    p.steps = (nsteps + splits - 1) / splits;
+    const dim3 grid((unsigned)((tiles + 7) / 8 * 8), (unsigned)((nsteps + p.steps - 1) / p.steps));
+    hipLaunchKernelGGL((w4_gemm_kernel<T, BWD, EPI, BM, BN, WGM, WGN>), grid, dim3(64 * WGM * WGN), 0, st, p);
+    return hipGetLastError();
+}
+
+template <int T, bool BWD, int EPI>
+hipError_t pick(const W4GemmParams& p, int64_t splits, hipStream_t st) {
+    if (p.M <= 64) return run<T, BWD, EPI, 64, 128, 2, 2>(p, splits, st);
+    if (p.M <= 512) return run<T, BWD, EPI, 128, 128, 2, 2>(p, splits, st);
+    return run<T, BWD, EPI, 256, 256, 2, 4>(p, splits, st);
+}
+
+template <int EPI>
+hipError_t pick_dtype(int dtype, const W4GemmParams& p, hipStream_t st) {
+    return dtype == kFp16 ? pick<kFp16, false, EPI>(p, 1, st) : pick<kBf16, false, EPI>(p, 1, st);
+}
+
+}  // namespace
+
+hipError_t launch_gemv_w4(const W4LinearArgs& a, hipStream_t st) {
+    W4GemmParams p{};
+    p.x = a.x; p.ldx = a.ldx; p.M = a.M; p.R = a.w.K; p.C = a.w.N; p.w = a.w;
+    p.bias = a.bias; p.y = a.y; p.ldy = a.ldy;
+    return pick_dtype<kW4Store>(a.dtype, p, st);
+}
+
+hipError_t launch_glu_w4(const W4GluArgs& a, hipStream_t st) {
+    W4GemmParams p{};
+    p.x = a.x; p.ldx = a.ldx; p.M = a.M; p.R = a.w.K; p.C = a.I; p.w = a.w; p.I = a.I;
+    p.y = a.y; p.ldy = a.ldy; p.gu = a.gu; p.ldgu = a.ldgu; p.dy = a.dy; p.lddy = a.lddy; p.act = a.act;
+    return a.dy ? pick_dtype<kW4GluBwd>(a.dtype, p, st) : pick_dtype<kW4Glu>(a.dtype, p, st);
+}
+
+// Splits of the reduction over N, so that a short batch still fills the 256
+// compute units; the partial sums go through the workspace.
+static int64_t bwd_splits(int64_t M, int64_t N, int64_t K) {
+    const int64_t bm = M <= 64 ? 64 : (M <= 512 ? 128 : 256), bn = M <= 512 ? 128 : 256;
+    const int64_t tiles = ((M + bm - 1) / bm) * ((K + bn - 1) / bn), steps = (N + 63) / 64;
+    int64_t s = 256 / tiles;
+    if (s > steps / 4) s = steps / 4;  // at least four steps a split
+    return s < 1 ? 1 : s;
+}
+
+size_t w4_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    const int64_t s = bwd_splits(M, N, K);
+    return s > 1 ? (size_t)(s * M * K) * 4 : 0;
+}
+
+hipError_t launch_gemv_w4_bwd(const W4BwdArgs& a, hipStream_t st) {
+    W4GemmParams p{};
+    p.x = a.dy; p.ldx = a.lddy; p.M = a.M; p.R = a.w.N; p.C = a.w.K; p.w = a.w;
+    p.y = a.dx; p.ldy = a.lddx; p.part = a.part;
+    const int64_t splits = bwd_splits(a.M, a.w.N, a.w.K);
+    if (splits <= 1)
+        return a.dtype == kFp16 ? pick<kFp16, true, kW4Store>(p, 1, st) : pick<kBf16, true, kW4Store>(p, 1, st);
+    const hipError_t e = a.dtype == kFp16 ? pick<kFp16, true, kW4Part>(p, splits, st)
+                                          : pick<kBf16, true, kW4Part>(p, splits, st);
+    if (e != hipSuccess) return e;
+    const int64_t nsteps = (p.R + 63) / 64, per = (nsteps + splits - 1) / splits;
+    const int real = (int)((nsteps + per - 1) / per);
+    const dim3 grid((unsigned)((a.M * (a.w.K / 4) + 255) / 256));
+    if (a.dtype == kFp16)
+        hipLaunchKernelGGL(w4_reduce_kernel<kFp16>, grid, dim3(256), 0, st, a.part, a.M, a.w.K, real, a.dx, a.lddx);
+    else
+        hipLaunchKernelGGL(w4_reduce_kernel<kBf16>, grid, dim3(256), 0, st, a.part, a.M, a.w.K, real, a.dx, a.lddx);
+    return hipGetLastError();
+}
+
+hipError_t launch_gate_bwd(const W4GateBwdArgs& a, hipStream_t st) {
+    const bool vec = a.I % 8 == 0 && (((uintptr_t)a.dy | (uintptr_t)a.gu | (uintptr_t)a.dgu) & 15) == 0 &&
+                     (a.lddy | a.ldgu | a.lddgu) % 8 == 0;
+    const int64_t n = a.M * (vec ? a.I / 8 : a.I);
+    const dim3 grid((unsigned)((n + 255) / 256));
+    if (a.dtype == kFp16) {
+        if (vec) hipLaunchKernelGGL((w4_gate_bwd_kernel<kFp16, 8>), grid, dim3(256), 0, st, a);
+        else hipLaunchKernelGGL((w4_gate_bwd_kernel<kFp16, 1>), grid, dim3(256), 0, st, a);
+    } else {
+        if (vec) hipLaunchKernelGGL((w4_gate_bwd_kernel<kBf16, 8>), grid, dim3(256), 0, st, a);
+        else hipLaunchKernelGGL((w4_gate_bwd_kernel<kBf16, 1>), grid, dim3(256), 0, st, a);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace qlin
