@@ -1,4 +1,5 @@
 // w4_gemm.hip -- launchers of the 4-bit weight GEMM (w4_gemm.hpp).
+#include "w4_dec_launch.hpp"
 #include "w4_gemm.hpp"
 
 namespace qlin {
@@ -28,9 +29,26 @@ hipError_t pick_dtype(int dtype, const W4GemmParams& p, hipStream_t st) {
     return dtype == kFp16 ? pick<kFp16, false, EPI>(p, 1, st) : pick<kBf16, false, EPI>(p, 1, st);
 }
 
+// few tokens: the streaming kernels
+hipError_t run_dec(int dtype, W4DecParams p, bool glu, hipStream_t st) {
+    p.pieces = (int)((p.w.K + 127) / 128);
+    const bool whole = p.w.group % 128 == 0;
+    const uint32_t r = (uint32_t)(p.w.group / (whole ? 128 : 32));
+    // unit / r by multiplication: exact for unit * r < 2^32 (both at most 2^15)
+    p.ratio_magic = r == 1 ? 0 : (uint32_t)(((1ull << 32) + r - 1) / r);
+    if (dtype == kFp16) return whole ? w4_dec_fp16_128(p, glu, st) : w4_dec_fp16_32(p, glu, st);
+    return whole ? w4_dec_bf16_128(p, glu, st) : w4_dec_bf16_32(p, glu, st);
+}
+
 }  // namespace
 
 hipError_t launch_gemv_w4(const W4LinearArgs& a, hipStream_t st) {
+    if (a.M <= kW4DecMaxM) {
+        W4DecParams d{};
+        d.x = a.x; d.ldx = a.ldx; d.M = (int)a.M; d.w = a.w; d.C = a.w.N;
+        d.bias = a.bias; d.y = a.y; d.ldy = a.ldy;
+        return run_dec(a.dtype, d, false, st);
+    }
     W4GemmParams p{};
     p.x = a.x; p.ldx = a.ldx; p.M = a.M; p.R = a.w.K; p.C = a.w.N; p.w = a.w;
     p.bias = a.bias; p.y = a.y; p.ldy = a.ldy;
@@ -38,6 +56,12 @@ hipError_t launch_gemv_w4(const W4LinearArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_glu_w4(const W4GluArgs& a, hipStream_t st) {
+    if (a.M <= kW4DecMaxM) {
+        W4DecParams d{};
+        d.x = a.x; d.ldx = a.ldx; d.M = (int)a.M; d.w = a.w; d.I = a.I; d.C = a.I;
+        d.y = a.y; d.ldy = a.ldy; d.gu = a.gu; d.ldgu = a.ldgu; d.dy = a.dy; d.lddy = a.lddy; d.act = a.act;
+        return run_dec(a.dtype, d, true, st);
+    }
     W4GemmParams p{};
     p.x = a.x; p.ldx = a.ldx; p.M = a.M; p.R = a.w.K; p.C = a.I; p.w = a.w; p.I = a.I;
     p.y = a.y; p.ldy = a.ldy; p.gu = a.gu; p.ldgu = a.ldgu; p.dy = a.dy; p.lddy = a.lddy; p.act = a.act;
