@@ -24,10 +24,10 @@ LIB = os.path.join(PKG, "libqlin.so")
 
 SOURCES = ["gemv.hip", "ks_i8.hip", "ks_f8.hip", "ks_w8a8_e4m3.hip", "ks_w8a8_e5m2.hip", "qlin_api.hip",
            "act_quant.hip", "qlin_w4_api.hip", "w4_gemm.hip",
-           "w4_dec_bf16_128.hip", "w4_dec_bf16_32.hip", "w4_dec_fp16_128.hip", "w4_dec_fp16_32.hip", "gemm.hip", "moe.hip", "moe_prefill.hip", "routing.hip"]
+           "w4_few_bf16.hip", "w4_few_fp16.hip", "w4_mid.hip", "gemm.hip", "moe.hip", "moe_prefill.hip", "routing.hip"]
 HEADERS = ["qlin_device.hpp", "qlin_launch.hpp", "gemv_kernels.hpp", "mfma_kernels.hpp", "ks_kernels.hpp",
            "ks_launch.hpp", "gemm_kernels.hpp", "w4_device.hpp", "w4_launch.hpp", "w4_gemm.hpp",
-           "w4_dec.hpp", "w4_dec_launch.hpp"]
+           "w4_mid.hpp", "w4_few.hpp", "w4_few_launch.hpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -96,6 +96,9 @@ struct W4Scale<kFp16> {
     }
 };
 
+// 16 zero bytes: the source of direct-to-LDS loads past the end of a row
+__device__ const u32x4_t kW4Zero16 = {0u, 0u, 0u, 0u};
+
 // ---------------------------------------------------------------- matrix instructions on 16-bit storage
 template <int T>
 __device__ __forceinline__ f32x16v_t mfma32(const u32x4_t& a, const u32x4_t& b, const f32x16v_t& c) {
@@ -115,6 +118,59 @@ __device__ __forceinline__ f32x4v_t mfma16(const u32x4_t& a, const u32x4_t& b, c
     else
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b),
                                                       c, 0, 0, 0);
+}
+
+// ---------------------------------------------------------------- operands and exchanges of the decode kernels
+__device__ __forceinline__ u32x4_t even_odd(const u32x4_t& v) {  // elements 0 2 4 6 1 3 5 7, the order codes unpack in
+    return u32x4_t{__builtin_amdgcn_perm(v.y, v.x, 0x05040100u), __builtin_amdgcn_perm(v.w, v.z, 0x05040100u),
+                   __builtin_amdgcn_perm(v.y, v.x, 0x07060302u), __builtin_amdgcn_perm(v.w, v.z, 0x07060302u)};
+}
+
+template <int T>
+__device__ __forceinline__ u32x4_t unpack8(uint32_t d) {
+    const uint32_t e = d & 0x0F0F0F0Fu, o = (d >> 4) & 0x0F0F0F0Fu;
+    return u32x4_t{codes2<T, false>(e), codes2<T, true>(e), codes2<T, false>(o), codes2<T, true>(o)};
+}
+
+__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {  // a's lanes 32.. <-> b's lanes ..31
+    typedef unsigned u2_t __attribute__((ext_vector_type(2)));
+    const u2_t r = __builtin_bit_cast(u2_t, __builtin_amdgcn_permlane32_swap(a, b, false, false));
+    a = r[0];
+    b = r[1];
+}
+
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {  // a's odd rows of 16 lanes <-> b's even rows
+    typedef unsigned u2_t __attribute__((ext_vector_type(2)));
+    const u2_t r = __builtin_bit_cast(u2_t, __builtin_amdgcn_permlane16_swap(a, b, false, false));
+    a = r[0];
+    b = r[1];
+}
+
+// v of lane group 0..3 in every lane: out[i] = v of lanes 16i..16i+15
+__device__ __forceinline__ void spread4(uint32_t v, uint32_t (&out)[4]) {
+    uint32_t a = v, b = v;
+    swap32(a, b);
+    out[0] = a;
+    out[1] = a;
+    out[2] = b;
+    out[3] = b;
+    swap16(out[0], out[1]);
+    swap16(out[2], out[3]);
+}
+
+// ---------------------------------------------------------------- waits
+// LDS writes of the workgroup become visible; outstanding global loads stay in flight
+__device__ __forceinline__ void w4_lds_barrier() {
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+template <int N_>
+__device__ __forceinline__ void w4_wait_vmcnt() {  // s_waitcnt vmcnt(N_), other counters untouched
+    static_assert(N_ >= 0 && N_ < 64, "vmcnt field");
+    __builtin_amdgcn_s_waitcnt((N_ & 15) | ((N_ >> 4) << 14) | 0x70 | 0xF00);
 }
 
 // ---------------------------------------------------------------- gate activations

@@ -1,5 +1,6 @@
 // w4_gemm.hip -- launchers of the 4-bit weight GEMM (w4_gemm.hpp).
-#include "w4_dec_launch.hpp"
+#include "w4_few_launch.hpp"
+#include "w4_mid_launch.hpp"
 #include "w4_gemm.hpp"
 
 namespace qlin {
@@ -29,25 +30,43 @@ hipError_t pick_dtype(int dtype, const W4GemmParams& p, hipStream_t st) {
     return dtype == kFp16 ? pick<kFp16, false, EPI>(p, 1, st) : pick<kBf16, false, EPI>(p, 1, st);
 }
 
-// few tokens: the streaming kernels
-hipError_t run_dec(int dtype, W4DecParams p, bool glu, hipStream_t st) {
-    p.pieces = (int)((p.w.K + 127) / 128);
-    const bool whole = p.w.group % 128 == 0;
-    const uint32_t r = (uint32_t)(p.w.group / (whole ? 128 : 32));
-    // unit / r by multiplication: exact for unit * r < 2^32 (both at most 2^15)
-    p.ratio_magic = r == 1 ? 0 : (uint32_t)(((1ull << 32) + r - 1) / r);
-    if (dtype == kFp16) return whole ? w4_dec_fp16_128(p, glu, st) : w4_dec_fp16_32(p, glu, st);
-    return whole ? w4_dec_bf16_128(p, glu, st) : w4_dec_bf16_32(p, glu, st);
+// fold units (of 128, 64 or 32 elements) per group r: unit / r by multiplication, exact for
+// unit * r < 2^32 (both at most 2^15); 0: r = 1
+uint32_t ratio_magic(int64_t group, int unit) {
+    const uint64_t r = (uint64_t)(group / unit);
+    return r == 1 ? 0 : (uint32_t)(((1ull << 32) + r - 1) / r);
+}
+
+hipError_t run_few(int dtype, W4FewParams p, const W4FewPlan& pl, hipStream_t st) {
+    p.rows = pl.rows;
+    p.passes = pl.passes;
+    p.groups = (int)(p.w.K / p.w.group);
+    p.ratio_magic = ratio_magic(p.w.group, p.w.group % 128 == 0 ? 128 : (p.w.group % 64 == 0 ? 64 : 32));
+    return dtype == kFp16 ? w4_few_fp16(p, pl, st) : w4_few_bf16(p, pl, st);
+}
+
+hipError_t run_mid(int dtype, W4MidParams p, const W4MidPlan& pl, hipStream_t st) {
+    p.groups = (int)(p.w.K / p.w.group);
+    p.ratio_magic = ratio_magic(p.w.group, 32);
+    return w4_mid(dtype, p, pl, st);
 }
 
 }  // namespace
 
 hipError_t launch_gemv_w4(const W4LinearArgs& a, hipStream_t st) {
-    if (a.M <= kW4DecMaxM) {
-        W4DecParams d{};
+    W4FewPlan pl;
+    if (w4_few_plan(a.M, a.w.K, a.w.group, a.w.N, false, pl)) {
+        W4FewParams d{};
         d.x = a.x; d.ldx = a.ldx; d.M = (int)a.M; d.w = a.w; d.C = a.w.N;
         d.bias = a.bias; d.y = a.y; d.ldy = a.ldy;
-        return run_dec(a.dtype, d, false, st);
+        return run_few(a.dtype, d, pl, st);
+    }
+    W4MidPlan mp;
+    if (w4_mid_plan(a.M, a.w.K, a.w.group, a.w.N, false, mp)) {
+        W4MidParams d{};
+        d.x = a.x; d.ldx = a.ldx; d.M = (int)a.M; d.w = a.w; d.C = a.w.N;
+        d.bias = a.bias; d.y = a.y; d.ldy = a.ldy;
+        return run_mid(a.dtype, d, mp, st);
     }
     W4GemmParams p{};
     p.x = a.x; p.ldx = a.ldx; p.M = a.M; p.R = a.w.K; p.C = a.w.N; p.w = a.w;
@@ -56,11 +75,19 @@ hipError_t launch_gemv_w4(const W4LinearArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_glu_w4(const W4GluArgs& a, hipStream_t st) {
-    if (a.M <= kW4DecMaxM) {
-        W4DecParams d{};
+    W4FewPlan pl;
+    if (w4_few_plan(a.M, a.w.K, a.w.group, a.I, true, pl)) {
+        W4FewParams d{};
         d.x = a.x; d.ldx = a.ldx; d.M = (int)a.M; d.w = a.w; d.I = a.I; d.C = a.I;
         d.y = a.y; d.ldy = a.ldy; d.gu = a.gu; d.ldgu = a.ldgu; d.dy = a.dy; d.lddy = a.lddy; d.act = a.act;
-        return run_dec(a.dtype, d, true, st);
+        return run_few(a.dtype, d, pl, st);
+    }
+    W4MidPlan mp;
+    if (w4_mid_plan(a.M, a.w.K, a.w.group, a.I, true, mp)) {
+        W4MidParams d{};
+        d.x = a.x; d.ldx = a.ldx; d.M = (int)a.M; d.w = a.w; d.I = a.I; d.C = a.I;
+        d.y = a.y; d.ldy = a.ldy; d.gu = a.gu; d.ldgu = a.ldgu; d.dy = a.dy; d.lddy = a.lddy; d.act = a.act;
+        return run_mid(a.dtype, d, mp, st);
     }
     W4GemmParams p{};
     p.x = a.x; p.ldx = a.ldx; p.M = a.M; p.R = a.w.K; p.C = a.I; p.w = a.w; p.I = a.I;

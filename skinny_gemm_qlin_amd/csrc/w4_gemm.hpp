@@ -39,9 +39,6 @@ struct W4GemmParams {
     float* part; int64_t steps;                 // 64-deep steps per split (gridDim.y splits)
 };
 
-// 16 zero bytes: the source of direct-to-LDS loads past the end of a row
-__device__ const u32x4_t kW4Zero16 = {0u, 0u, 0u, 0u};
-
 __device__ __forceinline__ void w4_stage_barrier() {
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     __builtin_amdgcn_s_waitcnt(0x70);  // vmcnt(0) lgkmcnt(0): this wave's loads into LDS and LDS writes are done
