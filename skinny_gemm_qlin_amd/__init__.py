@@ -13,8 +13,6 @@ torch.uint8 (a torch.float8_e4m3fn tensor may be passed for E4M3 codes).
 """
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from ._lib import (QLIN_ACT_GELU_TANH, QLIN_ACT_SILU, QLIN_DT_BF16, QLIN_DT_FP16, QLIN_FMT_E4M3,  # noqa: F401
@@ -33,15 +31,6 @@ def _stream(t: torch.Tensor, stream):
     if stream is None:
         return torch.cuda.current_stream(t.device).cuda_stream
     return getattr(stream, "cuda_stream", stream)
-
-
-_NO_SWITCH = contextlib.nullcontext()
-
-
-def _on(t: torch.Tensor):
-    """The device of `t` made current (kernels are launched on the current device)."""
-    d = t.device
-    return _NO_SWITCH if d.index is None or d.index == torch.cuda.current_device() else torch.cuda.device(d)
 
 
 def _need(t: torch.Tensor, name: str, dtypes, dims: int):
@@ -386,53 +375,79 @@ def qlin_moe_ffn_mxfp4(x, wr, w13, s13, w2, s2, topk, alpha=1.0, limit=10.0, y=N
     return y, ids, gw, logits, act
 
 
+# ----------------------------------------------------------------------------- 4-bit weights with group scales
+# One token through a small layer is a few microseconds on the GPU, so these calls look at each tensor
+# only as often as the checks need; _w4_weight says what was wrong once a check has failed.
+
 _DT16 = {torch.bfloat16: QLIN_DT_BF16, torch.float16: QLIN_DT_FP16}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_U8_ONLY = torch.uint8
 
 
 def _w4_weight(a, name, w, ws, wz):
-    """Checks a 4-bit weight against the 16-bit operand `a`; returns (N, K, group, dtype flag)."""
+    """Checks a 4-bit weight against the 16-bit operand `a`; returns (N, K, group, dtype flag, device index)."""
     dt = _DT16.get(a.dtype)
+    if dt is not None and w.dim() == 2 and ws.dim() == 2 and a.dim() == 2:
+        N, Kh = w.shape
+        rows, groups = ws.shape
+        K, dev = 2 * Kh, a.get_device()
+        if (rows == N and groups > 0 and K % groups == 0 and w.dtype is _U8_ONLY and ws.dtype is a.dtype
+                and ws.is_contiguous() and w.get_device() == dev == ws.get_device() and dev >= 0
+                and (w.stride(1) == 1 or Kh == 1) and (a.stride(1) == 1 or a.shape[1] == 1)
+                and (wz is None or (wz.dtype is _U8_ONLY and wz.shape == ws.shape and wz.is_contiguous()
+                                    and wz.get_device() == dev))):
+            return N, K, K // groups, dt, dev
+    # something is wrong: say what
     if dt is None:
         raise TypeError(f"{name}: dtype {a.dtype} not in {tuple(_DT16)}")
     _need(a, name, (a.dtype,), 2)
     _need(w, "w", (torch.uint8,), 2)
     _need(ws, "ws", (a.dtype,), 2)
     N, Kh = w.shape
-    K, groups = 2 * Kh, ws.shape[1]
-    if ws.shape[0] != N or groups < 1 or K % groups or not ws.is_contiguous():
+    if ws.shape[0] != N or ws.shape[1] < 1 or (2 * Kh) % ws.shape[1] or not ws.is_contiguous():
         raise ValueError(f"ws must be contiguous [{N}, K / group], got {tuple(ws.shape)}")
     if wz is not None:
         _need(wz, "wz", (torch.uint8,), 2)
         if wz.shape != ws.shape or not wz.is_contiguous():
             raise ValueError(f"wz must be contiguous {tuple(ws.shape)}, got {tuple(wz.shape)}")
-    for t in (w, ws, wz):
-        if t is not None and t.device != a.device:
-            raise ValueError(f"weights on {t.device}, {name} on {a.device}")
-    return N, K, K // groups, dt
+    raise ValueError(f"w, ws and wz must be on {name}'s device, {a.device}")
 
 
 def _out16(t, name, like, rows, cols):
-    """An output of `like`'s type and device: allocated, or checked."""
+    """An operand or output of `like`'s type and device: allocated if None, or checked."""
     if t is None:
         return torch.empty((rows, cols), dtype=like.dtype, device=like.device)
+    if (t.dtype is like.dtype and t.dim() == 2 and t.shape[0] == rows and t.shape[1] == cols
+            and (t.stride(1) == 1 or cols == 1) and t.get_device() == like.get_device()):
+        return t
     _need(t, name, (like.dtype,), 2)
-    if tuple(t.shape) != (rows, cols) or t.device != like.device:
-        raise ValueError(f"{name} must be [{rows}, {cols}] on {like.device}, got {tuple(t.shape)} on {t.device}")
-    return t
+    raise ValueError(f"{name} must be [{rows}, {cols}] on {like.device}, got {tuple(t.shape)} on {t.device}")
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _pitch(t):
-    """Row pitch in elements (a single row has no pitch of its own)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+def _pitch(t, rows, cols):
+    """Row pitch in elements; a single row has none of its own: its length, rounded up to 8."""
+    return t.stride(0) if rows > 1 else (cols + 7) // 8 * 8
 
 
-def _pitch8(t):
-    """_pitch rounded up to 8 elements for a single row, whose stride may be anything."""
-    return t.stride(0) if t.shape[0] > 1 else (max(t.stride(0), t.shape[1]) + 7) // 8 * 8
+def _wpitch(w):
+    return w.stride(0) if w.shape[0] > 1 else w.shape[1]
+
+
+def _launch(fn, where, dev, stream, *args):
+    """fn(*args, stream) with `dev` current: kernels are launched on the current device."""
+    st = _raw_stream(dev) if stream is None else getattr(stream, "cuda_stream", stream)
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, st)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, st)
+    if rc != 0:
+        check(rc, where)
 
 
 def qlin_gemv_w4(x, w, ws, wz=None, bias=None, y=None, stream=None):
@@ -440,19 +455,17 @@ def qlin_gemv_w4(x, w, ws, wz=None, bias=None, y=None, stream=None):
     uint8 [N, K/2] (element 2i in the low nibble, any row pitch that is a
     multiple of 16); ws [N, K/group] of x's dtype; wz uint8 [N, K/group] or None
     (zero point 8); bias [N] of x's dtype or None.  Returns y [M, N]."""
-    N, K, group, dt = _w4_weight(x, "x", w, ws, wz)
-    M = x.shape[0]
-    if x.shape[1] != K:
-        raise ValueError(f"w has K={K}, x has K={x.shape[1]}")
+    N, K, group, dt, dev = _w4_weight(x, "x", w, ws, wz)
+    M, Kx = x.shape
+    if Kx != K:
+        raise ValueError(f"w has K={K}, x has K={Kx}")
     if bias is not None:
         _need(bias, "bias", (x.dtype,), 1)
-        if bias.shape[0] != N or bias.device != x.device:
+        if bias.shape[0] != N or bias.get_device() != dev:
             raise ValueError(f"bias must be [{N}] on {x.device}")
     y = _out16(y, "y", x, M, N)
-    with _on(x):
-        check(load().qlin_gemv_w4(x.data_ptr(), _pitch8(x), M, K, dt, w.data_ptr(), w.stride(0), N, ws.data_ptr(),
-                                  _ptr(wz), group, _ptr(bias), y.data_ptr(), _pitch(y), _stream(x, stream)),
-              "qlin_gemv_w4")
+    _launch(load().qlin_gemv_w4, "qlin_gemv_w4", dev, stream, x.data_ptr(), _pitch(x, M, K), M, K, dt, w.data_ptr(),
+            _wpitch(w), N, ws.data_ptr(), _ptr(wz), group, _ptr(bias), y.data_ptr(), _pitch(y, M, N))
     return y
 
 
@@ -460,26 +473,32 @@ def qlin_gemv_w4_bwd_workspace_bytes(M: int, N: int, K: int) -> int:
     return int(load().qlin_gemv_w4_bwd_workspace_bytes(M, N, K))
 
 
-def _w4_workspace(workspace, M, N, K, like):
+def _w4_workspace(workspace, M, N, K, like, stream):
+    """The caller's workspace, or one allocated for the stream that the call runs on."""
     need = qlin_gemv_w4_bwd_workspace_bytes(M, N, K)
-    if workspace is None and need:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=like.device)
-    return (None, 0) if workspace is None else (workspace, workspace.numel() * workspace.element_size())
+    if workspace is None:
+        if not need:
+            return None, 0
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            raise ValueError(f"a raw stream needs a workspace of {need} bytes along with it")
+        with torch.cuda.stream(stream):  # None: the current one
+            workspace = torch.empty((need,), dtype=torch.uint8, device=like.device)
+    elif workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {like.device}")
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def qlin_gemv_w4_bwd(dy, w, ws, wz=None, dx=None, workspace=None, stream=None):
     """Input gradient of qlin_gemv_w4: dy [M, N] (row pitch a multiple of 8) and
     the weight -> dx [M, K]."""
-    N, K, group, dt = _w4_weight(dy, "dy", w, ws, wz)
-    M = dy.shape[0]
-    if dy.shape[1] != N:
-        raise ValueError(f"w has N={N}, dy has N={dy.shape[1]}")
+    N, K, group, dt, dev = _w4_weight(dy, "dy", w, ws, wz)
+    M, Ny = dy.shape
+    if Ny != N:
+        raise ValueError(f"w has N={N}, dy has N={Ny}")
     dx = _out16(dx, "dx", dy, M, K)
-    ws_buf, ws_bytes = _w4_workspace(workspace, M, N, K, dy)
-    with _on(dy):
-        check(load().qlin_gemv_w4_bwd(dy.data_ptr(), _pitch8(dy), M, N, dt, w.data_ptr(), w.stride(0), K,
-                                      ws.data_ptr(), _ptr(wz), group, dx.data_ptr(), _pitch(dx), _ptr(ws_buf),
-                                      ws_bytes, _stream(dy, stream)), "qlin_gemv_w4_bwd")
+    buf, size = _w4_workspace(workspace, M, N, K, dy, stream)
+    _launch(load().qlin_gemv_w4_bwd, "qlin_gemv_w4_bwd", dev, stream, dy.data_ptr(), _pitch(dy, M, N), M, N, dt,
+            w.data_ptr(), _wpitch(w), K, ws.data_ptr(), _ptr(wz), group, dx.data_ptr(), _pitch(dx, M, K), _ptr(buf), size)
     return dx
 
 
@@ -487,17 +506,17 @@ def qlin_glu_w4(x, w13, s13, z13=None, act=QLIN_ACT_SILU, y=None, gu=None, strea
     """Gated feed-forward front on 4-bit weights: w13 uint8 [2I, K/2] (gate rows,
     then up rows), s13 / z13 as ws / wz of qlin_gemv_w4.  Returns
     y = act(x Wg^T) * (x Wu^T) [M, I]; gu [M, 2I], if given, receives gate and up."""
-    N, K, group, dt = _w4_weight(x, "x", w13, s13, z13)
-    M, I = x.shape[0], N // 2
-    if x.shape[1] != K or N != 2 * I:
-        raise ValueError(f"w13 is [{N}, {K}], x has K={x.shape[1]}: rows must be 2I, K equal")
+    N, K, group, dt, dev = _w4_weight(x, "x", w13, s13, z13)
+    M, Kx = x.shape
+    I = N // 2
+    if Kx != K or N != 2 * I:
+        raise ValueError(f"w13 is [{N}, {K}], x has K={Kx}: rows must be 2I, K equal")
     y = _out16(y, "y", x, M, I)
     if gu is not None:
         _out16(gu, "gu", x, M, N)
-    with _on(x):
-        check(load().qlin_glu_w4(x.data_ptr(), _pitch8(x), M, K, dt, w13.data_ptr(), w13.stride(0), I, s13.data_ptr(),
-                                 _ptr(z13), group, int(act), y.data_ptr(), _pitch(y), _ptr(gu),
-                                 0 if gu is None else _pitch(gu), _stream(x, stream)), "qlin_glu_w4")
+    _launch(load().qlin_glu_w4, "qlin_glu_w4", dev, stream, x.data_ptr(), _pitch(x, M, K), M, K, dt, w13.data_ptr(),
+            _wpitch(w13), I, s13.data_ptr(), _ptr(z13), group, act, y.data_ptr(), _pitch(y, M, I), _ptr(gu),
+            0 if gu is None else _pitch(gu, M, N))
     return y
 
 
@@ -506,10 +525,10 @@ def qlin_glu_w4_bwd(dy, w13, s13, z13=None, act=QLIN_ACT_SILU, x=None, gu=None, 
     """Backward of qlin_glu_w4 from dy [M, I] and either the kept gu [M, 2I] or x
     [M, K] (gate and up are then recomputed).  Returns (dx [M, K], dgu [M, 2I]);
     need_dx=False skips the input gradient and returns (None, dgu)."""
-    N, K, group, dt = _w4_weight(dy, "dy", w13, s13, z13)
-    M, I = dy.shape[0], N // 2
-    if dy.shape[1] * 2 != N:
-        raise ValueError(f"w13 has {N} rows, dy has I={dy.shape[1]}")
+    N, K, group, dt, dev = _w4_weight(dy, "dy", w13, s13, z13)
+    M, I = dy.shape
+    if I * 2 != N:
+        raise ValueError(f"w13 has {N} rows, dy has I={I}")
     if x is None and gu is None:
         raise ValueError("either x or gu is needed")
     if x is not None:
@@ -520,16 +539,14 @@ def qlin_glu_w4_bwd(dy, w13, s13, z13=None, act=QLIN_ACT_SILU, x=None, gu=None, 
         dgu = torch.empty((M, (N + 7) // 8 * 8), dtype=dy.dtype, device=dy.device)[:, :N]
     else:
         _out16(dgu, "dgu", dy, M, N)
-    ws_buf, ws_bytes = None, 0
+    buf, size = None, 0
     if need_dx:
         dx = _out16(dx, "dx", dy, M, K)
-        ws_buf, ws_bytes = _w4_workspace(workspace, M, N, K, dy)
+        buf, size = _w4_workspace(workspace, M, N, K, dy, stream)
     else:
         dx = None
-    with _on(dy):
-        check(load().qlin_glu_w4_bwd(dy.data_ptr(), _pitch(dy), M, I, dt, int(act), _ptr(x),
-                                     0 if x is None else _pitch8(x), _ptr(gu), 0 if gu is None else _pitch(gu),
-                                     w13.data_ptr(), w13.stride(0), K, s13.data_ptr(), _ptr(z13), group,
-                                     dgu.data_ptr(), _pitch8(dgu), _ptr(dx), 0 if dx is None else _pitch(dx),
-                                     _ptr(ws_buf), ws_bytes, _stream(dy, stream)), "qlin_glu_w4_bwd")
+    _launch(load().qlin_glu_w4_bwd, "qlin_glu_w4_bwd", dev, stream, dy.data_ptr(), _pitch(dy, M, I), M, I, dt, act,
+            _ptr(x), 0 if x is None else _pitch(x, M, K), _ptr(gu), 0 if gu is None else _pitch(gu, M, N),
+            w13.data_ptr(), _wpitch(w13), K, s13.data_ptr(), _ptr(z13), group, dgu.data_ptr(), _pitch(dgu, M, N),
+            _ptr(dx), 0 if dx is None else _pitch(dx, M, K), _ptr(buf), size)
     return dx, dgu

@@ -7,12 +7,20 @@ namespace qlin {
 
 namespace {
 
+// fold units (of 128, 64 or 32 elements) per group r: unit / r by multiplication, exact for
+// unit * r < 2^32 (both at most 2^15); 0: r = 1
+uint32_t ratio_magic(int64_t group, int unit) {
+    const uint64_t r = (uint64_t)(group / unit);
+    return r == 1 ? 0 : (uint32_t)(((1ull << 32) + r - 1) / r);
+}
+
 template <int T, bool BWD, int EPI, int BM, int BN, int WGM, int WGN>
 hipError_t run(W4GemmParams p, int64_t splits, hipStream_t st) {
     constexpr int CT = EPI == kW4Glu || EPI == kW4GluBwd ? BN / 2 : BN;
     const int64_t tiles = ((p.M + BM - 1) / BM) * ((p.C + CT - 1) / CT);
     const int64_t nsteps = (p.R + 63) / 64;
     p.steps = (nsteps + splits - 1) / splits;
+    p.ratio_magic = ratio_magic(p.w.group, 32);
     const dim3 grid((unsigned)((tiles + 7) / 8 * 8), (unsigned)((nsteps + p.steps - 1) / p.steps));
     hipLaunchKernelGGL((w4_gemm_kernel<T, BWD, EPI, BM, BN, WGM, WGN>), grid, dim3(64 * WGM * WGN), 0, st, p);
     return hipGetLastError();
@@ -28,13 +36,6 @@ hipError_t pick(const W4GemmParams& p, int64_t splits, hipStream_t st) {
 template <int EPI>
 hipError_t pick_dtype(int dtype, const W4GemmParams& p, hipStream_t st) {
     return dtype == kFp16 ? pick<kFp16, false, EPI>(p, 1, st) : pick<kBf16, false, EPI>(p, 1, st);
-}
-
-// fold units (of 128, 64 or 32 elements) per group r: unit / r by multiplication, exact for
-// unit * r < 2^32 (both at most 2^15); 0: r = 1
-uint32_t ratio_magic(int64_t group, int unit) {
-    const uint64_t r = (uint64_t)(group / unit);
-    return r == 1 ? 0 : (uint32_t)(((1ull << 32) + r - 1) / r);
 }
 
 hipError_t run_few(int dtype, W4FewParams p, const W4FewPlan& pl, hipStream_t st) {

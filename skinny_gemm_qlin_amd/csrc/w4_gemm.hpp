@@ -37,6 +37,7 @@ struct W4GemmParams {
     const uint16_t* bias; uint16_t* y; int64_t ldy;
     uint16_t* gu; int64_t ldgu; const uint16_t* dy; int64_t lddy; int act;
     float* part; int64_t steps;                 // 64-deep steps per split (gridDim.y splits)
+    uint32_t ratio_magic;                       // forward: 32-K units per group r: unit / r = mulhi(unit, magic), 0: r = 1
 };
 
 __device__ __forceinline__ void w4_stage_barrier() {
@@ -46,6 +47,10 @@ __device__ __forceinline__ void w4_stage_barrier() {
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
+// Slot of 16-byte chunk c in LDS row r of 128 bytes: c ^ swz(r).  Two rows fill the 64 banks once, so pairs of
+// rows share a swizzle and 16 adjacent rows' copies of one chunk lie in different banks.
+__device__ __forceinline__ int w4_swz(int r) { return (r >> 1) & 7; }
+
 constexpr int64_t kW4BandM = 8;  // token tiles per raster band
 
 template <int T, bool BWD, int EPI, int BM, int BN, int WGM, int WGN>
@@ -54,11 +59,13 @@ __global__ __launch_bounds__(64 * WGM * WGN, 2) void w4_gemm_kernel(const W4Gemm
     constexpr bool kGlu = EPI == kW4Glu || EPI == kW4GluBwd;
     constexpr int TM = BM / WGM / 32, TN = BN / WGN / 32;  // 32 x 32 tiles per wave
     constexpr int BR = 64;                                 // reduction depth of a step
-    constexpr int XT = BM * BR * 2, WT = BN * BR * 2, ST = XT + WT;
+    constexpr int XT = BM * BR * 2, WT = BN * BR * 2;
     constexpr int XI = BM / 8 / NW;  // 1 KB loads per wave and step
     static_assert(2 * BN == NT, "one run of 32 codes per thread");
     static_assert(TM >= 1 && TN >= 1 && XI >= 1 && (!kGlu || (TN == 2 && !BWD)), "tile");
-    __shared__ __align__(16) uint8_t w4_lds[2 * ST];
+    // an object of its own for each tile: the compiler then knows that a load into one of them need not be
+    // waited for before another is read
+    __shared__ __align__(16) uint8_t x_even[XT], x_odd[XT], w_even[WT], w_odd[WT];
 
     const int64_t M = p.M, R = p.R, C = p.C;
     constexpr int CT = kGlu ? BN / 2 : BN;  // output columns per workgroup
@@ -72,18 +79,17 @@ __global__ __launch_bounds__(64 * WGM * WGN, 2) void w4_gemm_kernel(const W4Gemm
     const int64_t nsteps = (R + BR - 1) / BR;
     const int64_t s0 = (int64_t)blockIdx.y * p.steps, s1 = s0 + p.steps < nsteps ? s0 + p.steps : nsteps;
 
-    // ---- activation tile: LDS row r, slot c holds 16-byte chunk c ^ (r & 7)
+    // ---- activation tile
     const uint16_t* xsrc[XI];
     int xchunk[XI];
 #pragma unroll
     for (int i = 0; i < XI; ++i) {
         const int r = (wv * XI + i) * 8 + (lane >> 3);
         const int64_t m = m0 + r < M ? m0 + r : M - 1;  // rows past M: clamped, not stored
-        xchunk[i] = ((lane & 7) ^ (r & 7)) * 8;
+        xchunk[i] = ((lane & 7) ^ w4_swz(r)) * 8;
         xsrc[i] = p.x + m * p.ldx + xchunk[i];
     }
-    auto issue_x = [&](int64_t s, int slot) {
-        uint8_t* base = w4_lds + slot * ST;
+    auto issue_x = [&](int64_t s, uint8_t* base) {
 #pragma unroll
         for (int i = 0; i < XI; ++i) {
             const uint16_t* src = s * BR + xchunk[i] < R ? xsrc[i] + s * BR : (const uint16_t*)&kW4Zero16;
@@ -91,31 +97,46 @@ __global__ __launch_bounds__(64 * WGM * WGN, 2) void w4_gemm_kernel(const W4Gemm
         }
     };
 
-    // ---- this thread's run of 32 codes: one row, one group
+    // ---- this thread's run of 32 codes of a step: one row, one group
     const int64_t ngroups = p.w.K / p.w.group;
-    const uint8_t* wsrc;
-    const uint16_t* ssrc;
-    const uint8_t* zsrc;
-    int wdst;            // LDS offset of the run's first 16-byte piece (pieces placed below)
+    const bool has_z = p.w.wz != nullptr;
+    int wdst;            // LDS offset of the run's row or 64-byte block (pieces placed below)
     int run_r;           // its first reduction index inside a step
-    bool run_ok = true;  // the run's row / columns exist
-    int64_t grem = 0, gstep = 0;
+    int run_c = 0;       // backward: its 32-column block
+    int run_row = 0;     // forward: its LDS row
+    // forward.  A row gives 32 bytes to a step; loaded so, every 128-byte line would come from L2 four times.
+    // Four threads therefore load 64 bytes of a row, two steps' worth, of rows r and r' = BN / 2 + (r ^ 4), and
+    // exchange: threads 0, 1 keep row r, threads 2, 3 row r', each with one run of either step.
+    const uint8_t* wsrc[2];
+    const int j4 = tid & 3;
+    // forward: the scales of 4 groups at a time
+    const uint16_t* srow = nullptr;
+    const uint8_t* zrow = nullptr;
+    const bool wide = p.w.N * ngroups >= 4;
+    int left = 0;  // scales from the row's first to the matrix's last
+    // backward: the columns are fixed
+    const uint16_t* ssrc = nullptr;
+    const uint8_t* zsrc = nullptr;
+    bool run_ok = true;
     if constexpr (!BWD) {
-        const int r = tid >> 1, h = tid & 1;
-        int64_t n;
-        if constexpr (kGlu) {
-            const int64_t col = c0 + (r >> 6) * 32 + (r & 31);
-            n = (col < C ? col : C - 1) + ((r >> 5) & 1) * p.I;
-        } else {
-            n = c0 + r < C ? c0 + r : C - 1;
-        }
-        run_r = h * 32;
-        const int64_t k = s0 * BR + run_r, g = k / p.w.group;
-        grem = k - g * p.w.group;
-        wsrc = p.w.w + n * p.w.ldw;
-        ssrc = p.w.ws + n * ngroups + g;
-        zsrc = p.w.wz + (p.w.wz ? n * ngroups + g : 0);
-        wdst = r * (BR * 2);
+        auto matrix_row = [&](int r) -> int64_t {
+            if constexpr (kGlu) {
+                const int64_t col = c0 + (r >> 6) * 32 + (r & 31);
+                return (col < C ? col : C - 1) + ((r >> 5) & 1) * p.I;
+            } else {
+                return c0 + r < C ? c0 + r : C - 1;
+            }
+        };
+        const int ra = tid >> 2, rb = BN / 2 + ((tid >> 2) ^ 4);
+        run_row = j4 < 2 ? ra : rb;
+        run_r = (j4 & 1) * 32;
+        wsrc[0] = p.w.w + matrix_row(ra) * p.w.ldw;
+        wsrc[1] = p.w.w + matrix_row(rb) * p.w.ldw;
+        srow = p.w.ws + matrix_row(run_row) * ngroups;
+        const int64_t rest = (p.w.N - matrix_row(run_row)) * ngroups;
+        left = rest < (1 << 30) ? (int)rest : 1 << 30;
+        zrow = has_z ? p.w.wz + matrix_row(run_row) * ngroups : (const uint8_t*)srow;  // without zeros: not used
+        wdst = run_row * (BR * 2);
     } else {
         constexpr int RPR = BN / 32;  // runs per row
         const int r = tid / RPR, cc = tid % RPR;
@@ -123,43 +144,72 @@ __global__ __launch_bounds__(64 * WGM * WGN, 2) void w4_gemm_kernel(const W4Gemm
         run_ok = k < C;
         k = run_ok ? k : 0;
         run_r = r;
+        run_c = cc;
         const int64_t g = k / p.w.group;
-        wsrc = p.w.w + k / 2;
+        wsrc[0] = p.w.w + k / 2;
         ssrc = p.w.ws + g;
-        zsrc = p.w.wz + (p.w.wz ? g : 0);
+        zsrc = has_z ? p.w.wz + g : (const uint8_t*)ssrc;
         wdst = r * (BN * 2) + (cc ^ (r & 3)) * 64;
-        gstep = cc;
     }
     struct Codes { u32x4_t q; uint32_t s, z; };
-    auto load_codes = [&](int64_t s) {  // steps in order: s0, s0 + 1, ...
+    auto load_codes = [&](int64_t s) {  // backward
         Codes c;
-        const int64_t i = s * BR + run_r;
-        const bool ok = run_ok && i < R;
-        if constexpr (!BWD) {
-            c.q = *(const u32x4_t*)(wsrc + (ok ? i / 2 : 0));
-            c.s = ok ? *ssrc : 0;  // past the end of K: scale 0, weights 0
-            c.z = p.w.wz && ok ? *zsrc : 8;
-            grem += BR;
-#pragma unroll
-            for (int j = 0; j < 2; ++j)  // group >= 32: at most two groups a step
-                if (grem >= p.w.group && i + BR < R) {
-                    grem -= p.w.group;
-                    ++ssrc;
-                    zsrc += p.w.wz ? 1 : 0;
-                }
-        } else {
-            const int64_t n = i < R ? i : R - 1;
-            c.q = *(const u32x4_t*)(wsrc + n * p.w.ldw);
-            c.s = ok ? ssrc[n * ngroups] : 0;
-            c.z = p.w.wz ? zsrc[n * ngroups] : 8;
-        }
+        const int64_t i = s * BR + run_r, n = i < R ? i : R - 1;
+        c.q = *(const u32x4_t*)(wsrc[0] + n * p.w.ldw);
+        c.s = ssrc[n * ngroups];  // looked at when they are used, or this would wait for them
+        c.z = zsrc[n * ngroups];
         return c;
+    };
+    auto set_scale = [&](W4Scale<T>& sc, const Codes& c, int64_t s) {
+        sc.set(run_ok && s * BR + run_r < R ? c.s : 0, has_z ? c.z : 8);  // past the end: scale 0, weights 0
+    };
+    auto load_pair = [&](int64_t s, u32x4_t (&raw)[2]) {  // forward: the 128 K of steps s and s + 1
+        const int64_t k = s * BR + j4 * 32;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) raw[i] = *(const u32x4_t*)(wsrc[i] + (k < R ? k / 2 : 0));
+    };
+    auto exchange = [&](const u32x4_t (&raw)[2], u32x4_t& first, u32x4_t& second) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const uint32_t send = j4 < 2 ? raw[1][d] : raw[0][d];
+            const uint32_t got = (uint32_t)dpp_mov<0x4E>((int)send);  // quad_perm 2 3 0 1
+            first[d] = j4 < 2 ? raw[0][d] : got;
+            second[d] = j4 < 2 ? got : raw[1][d];
+        }
+    };
+    // forward: scales and zeros of groups 4v .. 4v + 3 of the run's row, as one load each.  The four may reach into
+    // the next row; at the end of the matrix they are its last four, and with fewer than four in all the first ones.
+    struct Window { uint2 s; uint32_t z; };
+    auto window_first = [&](int v) { return wide ? (v * 4 < left - 4 ? v * 4 : left - 4) : 0; };
+    auto load_window = [&](int v) {
+        Window w;
+        const int first = window_first(v);
+        if (wide) {
+            __builtin_memcpy(&w.s, srow + first, 8);
+            __builtin_memcpy(&w.z, zrow + first, 4);
+        } else {
+            const int b1 = left > 1 ? 1 : 0, b2 = left > 2 ? 2 : 0;
+            w.s = make_uint2((uint32_t)srow[0] | (uint32_t)srow[b1] << 16, srow[b2]);
+            w.z = (uint32_t)zrow[0] | (uint32_t)zrow[b1] << 8 | (uint32_t)zrow[b2] << 16;
+        }
+        return w;
+    };
+    auto group_of = [&](int64_t unit) {  // group of the 32 elements from 32 * unit; uniform
+        return p.ratio_magic ? (int)__umulhi((uint32_t)unit, p.ratio_magic) : (int)unit;
+    };
+    auto scale_of = [&](const Window& w, int v, int64_t s) {  // of this thread's run of step s
+        const int g0 = group_of(s * 2), g1 = group_of(s * 2 + 1), at = (run_r ? g1 : g0) - window_first(v);
+        const uint32_t d = at & 2 ? w.s.y : w.s.x;
+        W4Scale<T> sc;
+        sc.set(s * BR + run_r < R ? (d >> (16 * (at & 1))) & 0xFFFFu : 0u,  // past K: scale 0, weights 0
+               has_z ? (w.z >> (8 * (at & 3))) & 0xFFu : 8u);
+        return sc;
     };
     // piece i (8 weights) of the run
     auto put_piece = [&](uint8_t* wt, const W4Scale<T>& sc, const u32x4_t& q, int i) {
         int off;
-        if constexpr (!BWD) off = wdst + (((run_r >> 3) + i) ^ ((tid >> 1) & 7)) * 16;
-        else off = wdst + (i ^ (((int)gstep >> 1) & 3)) * 16;
+        if constexpr (!BWD) off = wdst + (((run_r >> 3) + i) ^ w4_swz(run_row)) * 16;
+        else off = wdst + (i ^ ((run_c >> 1) & 3) ^ (run_r & 1)) * 16;
         *(u32x4_t*)(wt + off) = sc.weights8(q[i]);
     };
 
@@ -167,14 +217,14 @@ __global__ __launch_bounds__(64 * WGM * WGN, 2) void w4_gemm_kernel(const W4Gemm
     auto frag_b = [&](const uint8_t* wt, int j, int ks) {
         if constexpr (!BWD) {
             const int r = wn * (BN / WGN) + j * 32 + row;
-            return *(const u32x4_t*)(wt + r * (BR * 2) + (((2 * ks + half) ^ (r & 7)) * 16));
+            return *(const u32x4_t*)(wt + r * (BR * 2) + (((2 * ks + half) ^ w4_swz(r)) * 16));
         } else {
             // lanes 4r..4r+3 of 16 lend their addresses to row r of a 4 x 16 block; lane i gets its column i
             typedef short s16x4_t __attribute__((ext_vector_type(4)));
             typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
             const int cc = wn * (BN / WGN / 32) + j, sub = lane & 15;
             const int piece = ((lane >> 4) & 1) * 2 + ((sub & 3) >> 1);
-            const int col = (cc ^ (sub >> 2)) * 64 + ((piece ^ ((cc >> 1) & 3)) * 16) + (sub & 1) * 8;
+            const int col = (cc ^ (sub >> 2)) * 64 + ((piece ^ ((cc >> 1) & 3) ^ ((sub >> 2) & 1)) * 16) + (sub & 1) * 8;
             const int r = ks * 16 + half * 8 + (sub >> 2);
             const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(wt + r * (BN * 2) + col));
             const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(wt + (r + 4) * (BN * 2) + col));
@@ -189,52 +239,119 @@ __global__ __launch_bounds__(64 * WGM * WGN, 2) void w4_gemm_kernel(const W4Gemm
 #pragma unroll
         for (int j = 0; j < TN; ++j) acc[i][j] = f32x16v_t{};
 
-    Codes cur = load_codes(s0);
-    issue_x(s0, 0);
-    {
-        W4Scale<T> sc;
-        sc.set(cur.s, cur.z);
+    u32x4_t fa[2][TM], fb[2][TN];  // operands of the current and the next 16-deep slice
+    auto load_frags = [&](int set, const uint8_t* xt, const uint8_t* wt, int ks) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) put_piece(w4_lds + XT, sc, cur.q, i);
-    }
-    if (s0 + 1 < s1) cur = load_codes(s0 + 1);
-    for (int64_t s = s0; s < s1; ++s) {
-        const int slot = (int)((s - s0) & 1);
-        w4_stage_barrier();  // tile s is complete for everyone, and everyone is done with tile s - 1
-        asm volatile("" : "+v"(cur.q), "+v"(cur.s), "+v"(cur.z));
-        const uint8_t* xt = w4_lds + slot * ST;
-        const uint8_t* wt = xt + XT;
-        if (s * BR + BR > R && (R & 7)) {  // backward, odd N: clear the last chunk's tail (whatever the row pitch holds)
+        for (int i = 0; i < TM; ++i) {
+            const int r = wm * (BM / WGM) + i * 32 + row;
+            fa[set][i] = *(const u32x4_t*)(xt + r * (BR * 2) + (((2 * ks + half) ^ w4_swz(r)) * 16));
+        }
+#pragma unroll
+        for (int j = 0; j < TN; ++j) fb[set][j] = frag_b(wt, j, ks);
+    };
+    auto multiply = [&](int set) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = mfma32<T>(fa[set][i], fb[set][j], acc[i][j]);
+    };
+    // backward, odd N: the last chunk of dy's rows is cleared past N (whatever the row pitch holds)
+    auto clear_tail = [&](int64_t s, uint8_t* xt) {
+        if (BWD && s * BR + BR > R && (R & 7) && s < s1) {
             const int e0 = (int)(R - s * BR), e1 = (e0 + 7) & ~7;
             for (int r = tid; r < BM; r += NT)
                 for (int e = e0; e < e1; ++e)
-                    *(uint16_t*)(w4_lds + slot * ST + r * (BR * 2) + (((e >> 3) ^ (r & 7)) * 16) + (e & 7) * 2) = 0;
+                    *(uint16_t*)(xt + r * (BR * 2) + (((e >> 3) ^ w4_swz(r)) * 16) + (e & 7) * 2) = 0;
             w4_stage_barrier();
         }
-        const bool more = s + 1 < s1;
-        if (more) issue_x(s + 1, slot ^ 1);
-        W4Scale<T> sc;
-        sc.set(cur.s, cur.z);
-        const u32x4_t q = cur.q;
-        if (s + 2 < s1) cur = load_codes(s + 2);
-        uint8_t* wnext = w4_lds + (slot ^ 1) * ST + XT;
+    };
+
+    // what is held for the next two steps' weights: backward their codes, forward the second run of a pair
+    // (while it is needed) and the next pair as loaded, and two windows of scales
+    Codes c1, c2;
+    u32x4_t q1, q2, raw[2];
+    Window win, next_win;
+    int v = 0;
+    (void)c1; (void)c2; (void)q1; (void)q2; (void)raw; (void)win; (void)next_win; (void)v;
+    W4Scale<T> sc;
+    if constexpr (BWD) {
+        const Codes c = load_codes(s0);
+        issue_x(s0, x_even);
+        c1 = load_codes(s0 + 1);
+        c2 = load_codes(s0 + 2);
+        set_scale(sc, c, s0);
 #pragma unroll
-        for (int ks = 0; ks < BR / 16; ++ks) {
-            u32x4_t a[TM], b[TN];
+        for (int i = 0; i < 4; ++i) put_piece(w_even, sc, c.q, i);
+    } else {
+        v = group_of(s0 * 2) >> 2;
+        win = load_window(v);
+        load_pair(s0, raw);
+        issue_x(s0, x_even);
+        u32x4_t q0;
+        exchange(raw, q0, q1);
+        sc = scale_of(win, v, s0);
 #pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                const int r = wm * (BM / WGM) + i * 32 + row;
-                a[i] = *(const u32x4_t*)(xt + r * (BR * 2) + (((2 * ks + half) ^ (r & 7)) * 16));
-            }
-#pragma unroll
-            for (int j = 0; j < TN; ++j) b[j] = frag_b(wt, j, ks);
-            if (more) put_piece(wnext, sc, q, ks);
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-#pragma unroll
-                for (int j = 0; j < TN; ++j) acc[i][j] = mfma32<T>(a[i], b[j], acc[i][j]);
-        }
+        for (int i = 0; i < 4; ++i) put_piece(w_even, sc, q0, i);
+        load_pair(s0 + 2, raw);
+        next_win = load_window(v + 1);
     }
+    // forward: the window of step s
+    auto turn_window = [&](int64_t s) {
+        const int want = group_of(s * 2) >> 2;
+        if (want != v) {  // uniform; the next one, since a window is at least 128 K
+            win = next_win;
+            v = want;
+            next_win = load_window(v + 1);
+        }
+    };
+    if constexpr (!BWD) turn_window(s0 + 1);
+    w4_stage_barrier();
+    clear_tail(s0, x_even);
+    load_frags(0, x_even, w_even, 0);
+    issue_x(s0 + 1 < s1 ? s0 + 1 : s0, x_odd);
+    // one step on tiles xt, wt; the next one's are xn, wn
+    auto step = [&](int64_t s, const bool odd, uint8_t* xt, uint8_t* wt, uint8_t* xn, uint8_t* wnext) {
+        // slices 0-2 of step s, with step s + 1's codes dequantised on the way; operands are read one slice ahead
+        u32x4_t q;
+        if constexpr (BWD) {
+            set_scale(sc, c1, s + 1);
+            q = c1.q;
+        } else {
+            sc = scale_of(win, v, s + 1);
+            q = q1;
+        }
+#pragma unroll
+        for (int ks = 0; ks < 3; ++ks) {
+            load_frags((ks + 1) & 1, xt, wt, ks + 1);
+            put_piece(wnext, sc, q, ks);
+            if (ks == 0) put_piece(wnext, sc, q, 3);
+            multiply(ks & 1);
+        }
+        // everyone's reads of step s and writes of step s + 1 are done, and its activation tile is there;
+        // the last slice's products run while the next step's operands are read
+        w4_stage_barrier();
+        clear_tail(s + 1, xn);
+        load_frags(0, xn, wnext, 0);
+        if constexpr (BWD) {
+            c1 = c2;
+            c2 = load_codes(s + 3);
+        } else {
+            if (!odd) {  // s + 2 opens a pair
+                exchange(raw, q1, q2);
+                load_pair(s + 4, raw);
+            } else {
+                q1 = q2;
+            }
+            turn_window(s + 2);
+        }
+        issue_x(s + 2 < s1 ? s + 2 : s, xt);  // past the end: the idle tile, again
+        multiply(1);
+    };
+    for (int64_t s = s0; s < s1; s += 2) {
+        step(s, false, x_even, w_even, x_odd, w_odd);
+        if (s + 1 < s1) step(s + 1, true, x_odd, w_odd, x_even, w_even);
+    }
+    w4_wait_vmcnt<0>();  // no load into LDS outlives the workgroup
 
     // ---- epilogue: register e of a 32 x 32 tile holds token 8(e/4) + 4*half + e%4, column lane%32
 #pragma unroll
