@@ -26,10 +26,23 @@ hipError_t run(W4GemmParams p, int64_t splits, hipStream_t st) {
     return hipGetLastError();
 }
 
+// Estimated time of the GEMM with square tiles.  A 64-deep step of a 256 x 256 tile takes 1.95 us (one workgroup a
+// compute unit), of a 128 x 128 tile 1.05 us alone on its unit and 1.2 to 1.4 us where two share one (2048 tokens,
+// 17408 x 5120, 80 steps: 544 large tiles 478 us, 2176 small ones 489 us; 509 tokens, 4096 x 7168, 112 steps: 32
+// large ones 203 us, 128 small ones 120 us; 256 tokens, 17408 x 5120, 272 small ones 120 us).
+float gemm_us(int64_t M, int64_t cols, int64_t R, int tile) {
+    const int64_t tiles = ((M + tile - 1) / tile) * ((cols + tile - 1) / tile), steps = (R + 63) / 64;
+    if (tile == 256) return 10.f + (float)((tiles + 255) / 256 * steps) * 1.95f;
+    const int64_t full = tiles / 512, rest = tiles - full * 512;
+    return 10.f + (float)steps * ((float)full * 1.22f + (rest == 0 ? 0.f : (rest <= 256 ? 1.05f : 1.4f)));
+}
+
 template <int T, bool BWD, int EPI>
 hipError_t pick(const W4GemmParams& p, int64_t splits, hipStream_t st) {
-    if (p.M <= 64) return run<T, BWD, EPI, 64, 128, 2, 2>(p, splits, st);
-    if (p.M <= 512) return run<T, BWD, EPI, 128, 128, 2, 2>(p, splits, st);
+    if (BWD && p.M <= 64) return run<T, BWD, EPI, 64, 128, 2, 2>(p, splits, st);
+    const int64_t cols = (EPI == kW4Glu || EPI == kW4GluBwd ? 2 : 1) * p.C;
+    if (BWD ? p.M <= 512 : gemm_us(p.M, cols, p.R, 128) < gemm_us(p.M, cols, p.R, 256))
+        return run<T, BWD, EPI, 128, 128, 2, 2>(p, splits, st);
     return run<T, BWD, EPI, 256, 256, 2, 4>(p, splits, st);
 }
 
@@ -44,6 +57,13 @@ hipError_t run_few(int dtype, W4FewParams p, const W4FewPlan& pl, hipStream_t st
     p.groups = (int)(p.w.K / p.w.group);
     p.ratio_magic = ratio_magic(p.w.group, p.w.group % 128 == 0 ? 128 : (p.w.group % 64 == 0 ? 64 : 32));
     return dtype == kFp16 ? w4_few_fp16(p, pl, st) : w4_few_bf16(p, pl, st);
+}
+
+// The kernel for 17 to 64 tokens also takes longer batches, in blocks of 64, where the GEMM's tiles would leave
+// compute units idle (128 tokens, 4096 x 7168: 22 us against 102), and matrices of fewer than four scales, which
+// the GEMM loads four at a time.
+bool use_mid(int64_t M, const W4Weight& w, const W4MidPlan& pl) {
+    return w.N * (w.K / w.group) < 4 || pl.us < fminf(gemm_us(M, w.N, w.K, 128), gemm_us(M, w.N, w.K, 256));
 }
 
 hipError_t run_mid(int dtype, W4MidParams p, const W4MidPlan& pl, hipStream_t st) {
@@ -63,7 +83,7 @@ hipError_t launch_gemv_w4(const W4LinearArgs& a, hipStream_t st) {
         return run_few(a.dtype, d, pl, st);
     }
     W4MidPlan mp;
-    if (w4_mid_plan(a.M, a.w.K, a.w.group, a.w.N, false, mp)) {
+    if (w4_mid_plan(a.M, a.w.K, a.w.group, a.w.N, false, mp) && use_mid(a.M, a.w, mp)) {
         W4MidParams d{};
         d.x = a.x; d.ldx = a.ldx; d.M = (int)a.M; d.w = a.w; d.C = a.w.N;
         d.bias = a.bias; d.y = a.y; d.ldy = a.ldy;
@@ -84,7 +104,7 @@ hipError_t launch_glu_w4(const W4GluArgs& a, hipStream_t st) {
         return run_few(a.dtype, d, pl, st);
     }
     W4MidPlan mp;
-    if (w4_mid_plan(a.M, a.w.K, a.w.group, a.I, true, mp)) {
+    if (w4_mid_plan(a.M, a.w.K, a.w.group, a.I, true, mp) && use_mid(a.M, a.w, mp)) {
         W4MidParams d{};
         d.x = a.x; d.ldx = a.ldx; d.M = (int)a.M; d.w = a.w; d.I = a.I; d.C = a.I;
         d.y = a.y; d.ldy = a.ldy; d.gu = a.gu; d.ldgu = a.ldgu; d.dy = a.dy; d.lddy = a.lddy; d.act = a.act;

@@ -1,9 +1,10 @@
-// w4_mid.hpp -- 4-bit weight products for 9 to 64 tokens: the linear layer
-// and the gated feed-forward front.
+// w4_mid.hpp -- 4-bit weight products for 17 to 64 tokens, and for more where
+// the matrix is too small for the GEMM's tiles (blocks of 64 tokens): the
+// linear layer and the gated feed-forward front.
 //
 // Bound: the weights' stream from HBM, the activations' from L2 (every
 // workgroup reads all of x, M K 2 bytes), and the vector unit's dequantisation
-// come out within a factor of two of each other; so a workgroup owns 32 or 64
+// come out within a factor of two of each other; so a workgroup owns 32 to 128
 // weight rows (gated: half of them gate, half up) for all tokens, the x of a
 // step is shared in LDS, and no weight is dequantised twice.
 //
@@ -14,7 +15,8 @@
 // 16 bytes, of which lane half h takes dwords 2h and 2h + 1, one for each of
 // two matrix instructions, and x is read in the same order.  Codes are
 // dequantised in registers on the way, rounded once to the 16-bit type.  The
-// waves' sums are added in wave order through LDS at the end.
+// waves' sums are added in wave order through LDS at the end, 16 or 8
+// tokens at a time.
 #pragma once
 #include "w4_device.hpp"
 #include "w4_launch.hpp"
@@ -41,15 +43,21 @@ inline __host__ __device__ uint32_t w4_mid_scales(int rows, int groups) {
     return ((uint32_t)(rows * groups * 2) + 15u) / 16u * 16u + ((uint32_t)(rows * groups) + 15u) / 16u * 16u + 128u;
 }
 
-template <int T, int MT, int NTL, int STAGES>
+template <int T, int MT, int NTL, int STAGES>  // 2 <= STAGES <= 4
 __global__ __launch_bounds__(512) void w4_mid_kernel(const W4MidParams p) {
     constexpr int BM = 32 * MT, BN = 32 * NTL, NW = 8, NT = 512, STEP = kW4MidStep;
     constexpr int XI = BM / 2 / NW;                   // x loads of a wave and step: 2 rows of 512 bytes each
     constexpr int WL = BN / 8;                        // code loads of a step: 8 rows of 128 bytes each
+    constexpr int WI = (WL + NW - 1) / NW;            // of a wave; the last only of waves below WL % NW
     constexpr int ST = w4_mid_stage<BM, BN>();
-    extern __shared__ __align__(16) uint8_t w4m_lds[];  // STAGES stages (later the sums), scales
+    extern __shared__ __align__(16) uint8_t w4m_lds[];  // scales
+    __shared__ __align__(16) uint8_t st0[ST], st1[ST], st2[STAGES > 2 ? ST : 16], st3[STAGES > 3 ? ST : 16];
+    constexpr int RT = NTL > 2 ? 8 : 16;                // tokens whose sums are added at a time
+    __shared__ float red[NW * RT * BN];                 // [wave][token % RT][row]
 
-    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, M = p.M, G = p.groups;
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, G = p.groups;
+    const int64_t m0 = (int64_t)blockIdx.y * BM;
+    const int M = p.M - m0 < BM ? (int)(p.M - m0) : BM;  // tokens of this workgroup
     const int K = (int)p.w.K, steps = (K + STEP - 1) / STEP;
     const bool glu = p.I > 0;
     const int CT = glu ? BN / 2 : BN;                 // columns of a workgroup
@@ -71,7 +79,7 @@ __global__ __launch_bounds__(512) void w4_mid_kernel(const W4MidParams p) {
                     __builtin_amdgcn_global_load_lds((const void*)((const uint8_t*)src + o + tid * 16),
                                                      (lds_void_t*)(w4m_lds + at + o + wv * 1024), 16, 0, 0);
         };
-        uint32_t at = STAGES * ST;
+        uint32_t at = 0;
         const uint32_t count = (uint32_t)CL * G;
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
@@ -100,21 +108,30 @@ __global__ __launch_bounds__(512) void w4_mid_kernel(const W4MidParams p) {
     for (int i = 0; i < XI; ++i) {
         const int r = (wv * XI + i) * 2 + (lane >> 5);
         xk[i] = ((lane & 31) ^ (r & 31)) * 8;
-        xsrc[i] = p.x + (r < M ? r : M - 1) * p.ldx + xk[i];
+        xsrc[i] = p.x + (m0 + (r < M ? r : M - 1)) * p.ldx + xk[i];
     }
-    const int wr = wv * 8 + (lane >> 3), wk = ((lane & 7) ^ (wr & 7)) * 32;
-    const uint8_t* wsrc = p.w.w + row_of(wr < BN ? wr : 0) * p.w.ldw + wk / 2;
-    auto issue = [&](int s) {
-        uint8_t* base = w4m_lds + (s % STAGES) * ST;
+    const uint8_t* wsrc[WI];
+    int wk[WI];
+#pragma unroll
+    for (int i = 0; i < WI; ++i) {
+        const int r = (i * NW + wv) * 8 + (lane >> 3);
+        wk[i] = ((lane & 7) ^ (r & 7)) * 32;
+        wsrc[i] = p.w.w + row_of(r < BN ? r : 0) * p.w.ldw + wk[i] / 2;
+    }
+    const bool full = WL % NW == 0 || wv < WL % NW;  // this wave has WI code loads, not WI - 1
+    auto issue = [&](int s, uint8_t* base) {
         const int k0 = s * STEP;
 #pragma unroll
         for (int i = 0; i < XI; ++i) {
             const void* src = k0 + xk[i] < K ? (const void*)(xsrc[i] + k0) : (const void*)&kW4Zero16;
             __builtin_amdgcn_global_load_lds(src, (lds_void_t*)(base + (wv * XI + i) * 1024), 16, 0, 0);
         }
-        if (WL >= NW || wv < WL)  // past K: zero codes, and x is zero there
-            __builtin_amdgcn_global_load_lds(k0 + wk < K ? (const void*)(wsrc + k0 / 2) : (const void*)&kW4Zero16,
-                                             (lds_void_t*)(base + BM * STEP * 2 + wv * 1024), 16, 0, 0);
+#pragma unroll
+        for (int i = 0; i < WI; ++i) {  // past K: zero codes, and x is zero there
+            const void* src = k0 + wk[i] < K ? (const void*)(wsrc[i] + k0 / 2) : (const void*)&kW4Zero16;
+            uint8_t* dst = base + BM * STEP * 2 + (i * NW + wv) * 1024;
+            if (i + 1 < WI || full) __builtin_amdgcn_global_load_lds(src, (lds_void_t*)dst, 16, 0, 0);
+        }
     };
 
     const int row = lane & 31, half = lane >> 5;
@@ -134,21 +151,16 @@ __global__ __launch_bounds__(512) void w4_mid_kernel(const W4MidParams p) {
 #pragma unroll
         for (int t = 0; t < NTL; ++t) acc[m][t] = f32x16v_t{};
 
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s)
-        if (s < steps) issue(s);
-    for (int s = 0; s < steps; ++s) {
+    // step s on stage `xt`; the stage that step s - 1 used is filled again
+    auto step = [&](int s, const uint8_t* xt, uint8_t* refill) {
         // this wave's loads of step s have arrived once at most those of the next STAGES - 2 steps are left
         if (s + STAGES - 2 < steps) {
-            constexpr int A = (STAGES - 2) * (XI + 1), B = (STAGES - 2) * XI;
-            if (WL >= NW || wv < WL) w4_wait_vmcnt<A>();
-            else w4_wait_vmcnt<B>();
+            if (full) w4_wait_vmcnt<(STAGES - 2) * (XI + WI)>();
+            else w4_wait_vmcnt<(STAGES - 2) * (XI + WI - 1)>();
         } else {
             w4_wait_vmcnt<0>();
         }
         w4_lds_barrier();  // step s is complete for everyone, and everyone is done with step s - 1
-        if (s + STAGES - 1 < steps) issue(s + STAGES - 1);
-        const uint8_t* xt = w4m_lds + (s % STAGES) * ST;
         const uint8_t* wt = xt + BM * STEP * 2;
         uint32_t g = (uint32_t)(s * (STEP / 32) + wv);
         if (p.ratio_magic) g = __umulhi(g, p.ratio_magic);
@@ -161,64 +173,80 @@ __global__ __launch_bounds__(512) void w4_mid_kernel(const W4MidParams p) {
                 const int r = m * 32 + row;
                 a[m][ks] = *(const u32x4_t*)(xt + r * (STEP * 2) + (((wv * 4 + 2 * half + ks) ^ (r & 31)) * 16));
             }
+        uint2 q[NTL];
+        W4Scale<T> sc[NTL];
 #pragma unroll
         for (int t = 0; t < NTL; ++t) {
             const int lr = lrow[t];
-            const uint2 q = *(const uint2*)(wt + lr * (STEP / 2) + ((wv ^ (lr & 7)) * 16) + half * 8);
-            W4Scale<T> sc;
-            sc.set(*(const uint16_t*)(w4m_lds + sbase[t] + g * 2), has_z ? w4m_lds[zbase[t] + g] : 8u);
-            const u32x4_t b0 = sc.weights8(q.x), b1 = sc.weights8(q.y);
+            q[t] = *(const uint2*)(wt + lr * (STEP / 2) + ((wv ^ (lr & 7)) * 16) + half * 8);
+            const uint32_t sv = *(const uint16_t*)(w4m_lds + sbase[t] + g * 2), zv = w4m_lds[zbase[t] + g];
+            sc[t].set(sv, has_z ? zv : 8u);
+        }
+        if (s + STAGES - 1 < steps) issue(s + STAGES - 1, refill);
+#pragma unroll
+        for (int t = 0; t < NTL; ++t) {
+            const u32x4_t b0 = sc[t].weights8(q[t].x), b1 = sc[t].weights8(q[t].y);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 acc[m][t] = mfma32<T>(a[m][0], b0, acc[m][t]);
                 acc[m][t] = mfma32<T>(a[m][1], b1, acc[m][t]);
             }
         }
-    }
-    w4_lds_barrier();  // the stages are no longer needed
-
-    // ---- sums of the waves, in order.  red[wave][token][BN]
-    float* red = (float*)w4m_lds;
+    };
+    uint8_t* const ring[4] = {st0, st1, st2, st3};
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int s = 0; s < STAGES - 1; ++s)
+        if (s < steps) issue(s, ring[s]);
+    for (int s = 0; s < steps; s += STAGES) {
+#pragma unroll
+        for (int i = 0; i < STAGES; ++i)
+            if (s + i < steps) step(s + i, ring[i], ring[(i + STAGES - 1) % STAGES]);
+    }
+
+    // ---- sums of the waves, in order, RT tokens at a time: register e of a tile is token 8(e/4) + 4*half + e%4
+#pragma unroll
+    for (int part = 0; part < BM / RT; ++part) {
+        if (part * RT >= M) break;  // workgroup-uniform
+        if (part > 0) w4_lds_barrier();
+        constexpr int PT = 32 / RT;  // parts of a tile
 #pragma unroll
         for (int t = 0; t < NTL; ++t)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int tok = m * 32 + 8 * (e >> 2) + 4 * half + (e & 3);
-                if (tok < M) red[(wv * BM + tok) * BN + t * 32 + row] = acc[m][t][e];
+            for (int e = 0; e < RT / 2; ++e) {
+                const int tok = 8 * (e >> 2) + 4 * half + (e & 3);
+                red[(wv * RT + tok) * BN + t * 32 + row] = acc[part / PT][t][(part % PT) * (RT / 2) + e];
             }
-    w4_lds_barrier();
-    auto total = [&](int m, int lr) {
-        float v = 0.f;
+        w4_lds_barrier();
+        auto total = [&](int m, int lr) {
+            float v = 0.f;
 #pragma unroll
-        for (int k = 0; k < NW; ++k) v += red[(k * BM + m) * BN + lr];
-        return v;
-    };
-    const int cols_log = glu ? (NTL == 2 ? 5 : 4) : (NTL == 2 ? 6 : 5);  // log2 CT
-    for (int o = tid; o < M << cols_log; o += NT) {
-        const int m = o >> cols_log, j = o & (CT - 1);
-        const int64_t c = c0 + j;
-        if (j >= CL) continue;
-        float v = total(m, j);
-        if (glu) {
-            const float v2 = total(m, CT + j);
-            float av, dav;
-            gate_act(v, p.act, av, dav);
-            if (!p.dy) {
-                p.y[m * p.ldy + c] = f32_to_h<T>(av * v2);
-                if (p.gu) {
-                    p.gu[m * p.ldgu + c] = f32_to_h<T>(v);
-                    p.gu[m * p.ldgu + p.I + c] = f32_to_h<T>(v2);
+            for (int k = 0; k < NW; ++k) v += red[(k * RT + m) * BN + lr];
+            return v;
+        };
+        for (int o = tid; o < RT * CT; o += NT) {
+            const int mm = glu ? o / (BN / 2) : o / BN, j = o - mm * CT;
+            const int64_t m = m0 + part * RT + mm, c = c0 + j;
+            if (j >= CL || part * RT + mm >= M) continue;
+            float v = total(mm, j);
+            if (glu) {
+                const float v2 = total(mm, CT + j);
+                float av, dav;
+                gate_act(v, p.act, av, dav);
+                if (!p.dy) {
+                    p.y[m * p.ldy + c] = f32_to_h<T>(av * v2);
+                    if (p.gu) {
+                        p.gu[m * p.ldgu + c] = f32_to_h<T>(v);
+                        p.gu[m * p.ldgu + p.I + c] = f32_to_h<T>(v2);
+                    }
+                } else {
+                    const float d = h_to_f32<T>(p.dy[m * p.lddy + c]);
+                    p.gu[m * p.ldgu + c] = f32_to_h<T>(d * v2 * dav);
+                    p.gu[m * p.ldgu + p.I + c] = f32_to_h<T>(d * av);
                 }
             } else {
-                const float d = h_to_f32<T>(p.dy[m * p.lddy + c]);
-                p.gu[m * p.ldgu + c] = f32_to_h<T>(d * v2 * dav);
-                p.gu[m * p.ldgu + p.I + c] = f32_to_h<T>(d * av);
+                if (p.bias) v += h_to_f32<T>(p.bias[c]);
+                p.y[m * p.ldy + c] = f32_to_h<T>(v);
             }
-        } else {
-            if (p.bias) v += h_to_f32<T>(p.bias[c]);
-            p.y[m * p.ldy + c] = f32_to_h<T>(v);
         }
     }
 }

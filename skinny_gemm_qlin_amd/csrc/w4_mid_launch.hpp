@@ -1,12 +1,11 @@
-// w4_mid_launch.hpp -- plan and launcher of the kernels for 9 to 64 tokens.
+// w4_mid_launch.hpp -- plan and launcher of the kernels for 17 to 64
+// tokens and for small matrices.
 #pragma once
 #include "w4_mid.hpp"
 
 namespace qlin {
 
-constexpr int kW4MidMaxM = 64;
-
-struct W4MidPlan { int ntl; uint32_t scales; };
+struct W4MidPlan { int ntl; uint32_t scales; float us; };  // row tiles, LDS of the scales, estimated time
 
 // false if the scales of 32 rows do not fit LDS next to two stages
 bool w4_mid_plan(int64_t M, int64_t K, int64_t group, int64_t C, bool glu, W4MidPlan& o);
