@@ -1,6 +1,7 @@
 // w4_gemm.hip -- launchers of the 4-bit weight GEMM (w4_gemm.hpp).
 #include "w4_few_launch.hpp"
 #include "w4_mid_launch.hpp"
+#include "w4_bwd.hpp"
 #include "w4_gemm.hpp"
 
 namespace qlin {
@@ -39,7 +40,6 @@ float gemm_us(int64_t M, int64_t cols, int64_t R, int tile) {
 
 template <int T, bool BWD, int EPI>
 hipError_t pick(const W4GemmParams& p, int64_t splits, hipStream_t st) {
-    if (BWD && p.M <= 64) return run<T, BWD, EPI, 64, 128, 2, 2>(p, splits, st);
     const int64_t cols = (EPI == kW4Glu || EPI == kW4GluBwd ? 2 : 1) * p.C;
     if (BWD ? p.M <= 512 : gemm_us(p.M, cols, p.R, 128) < gemm_us(p.M, cols, p.R, 256))
         return run<T, BWD, EPI, 128, 128, 2, 2>(p, splits, st);
@@ -116,39 +116,76 @@ hipError_t launch_glu_w4(const W4GluArgs& a, hipStream_t st) {
     return a.dy ? pick_dtype<kW4GluBwd>(a.dtype, p, st) : pick_dtype<kW4Glu>(a.dtype, p, st);
 }
 
-// Splits of the reduction over N, so that a short batch still fills the 256
-// compute units; the partial sums go through the workspace.
-static int64_t bwd_splits(int64_t M, int64_t N, int64_t K) {
-    const int64_t bm = M <= 64 ? 64 : (M <= 512 ? 128 : 256), bn = M <= 512 ? 128 : 256;
-    const int64_t tiles = ((M + bm - 1) / bm) * ((K + bn - 1) / bn), steps = (N + 63) / 64;
-    int64_t s = 256 / tiles;
-    if (s > steps / 4) s = steps / 4;  // at least four steps a split
-    return s < 1 ? 1 : s;
+// How the input gradient is laid out: shares of the reduction over N, so that short batches and narrow outputs
+// fill the chip too; the shares' partial sums go through the workspace.
+namespace {
+
+struct BwdPlan { int cw; int64_t shares, per; };  // cw: codes of a lane (up to 64 tokens), 0: the GEMM; per: blocks or steps
+
+BwdPlan bwd_plan(int64_t M, int64_t N, int64_t K) {
+    BwdPlan o{};
+    if (M <= 64) {
+        o.cw = M <= 32 ? 16 : 8;
+        const int64_t cols = (K + 16 * o.cw - 1) / (16 * o.cw), blocks = (N + 31) / 32;
+        // about 1024 workgroups of 4 waves, at least one block a wave
+        int64_t shares = 512 / cols;
+        if (shares > (blocks + 3) / 4) shares = (blocks + 3) / 4;
+        o.per = shares > 1 ? (blocks + shares - 1) / shares : blocks;
+        o.shares = (blocks + o.per - 1) / o.per;
+        return o;
+    }
+    const int64_t tile = M <= 512 ? 128 : 256, tiles = ((M + tile - 1) / tile) * ((K + tile - 1) / tile);
+    const int64_t steps = (N + 63) / 64;
+    float best = 0.f;
+    for (int64_t s = 1; s <= 8 && (s == 1 || steps / s >= 4); ++s) {
+        // a step of a 256 x 256 tile 1.8 us, of a 128 x 128 tile 1.1 us; partial sums at 4 TB/s, written and read
+        const float us = (float)((tiles * s + 255) / 256 * ((steps + s - 1) / s)) * (tile == 256 ? 1.8f : 1.1f) +
+                         (s > 1 ? 5.f + (float)(s * M * K) * 8e-6f / 4.f : 0.f);
+        if (s > 1 && us >= best) continue;
+        best = us;
+        o.per = (steps + s - 1) / s;
+        o.shares = (steps + o.per - 1) / o.per;
+    }
+    return o;
 }
 
-size_t w4_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-    const int64_t s = bwd_splits(M, N, K);
-    return s > 1 ? (size_t)(s * M * K) * 4 : 0;
+template <int T>
+hipError_t run_bwd(const W4BwdArgs& a, const BwdPlan& pl, hipStream_t st) {
+    W4BwdParams p{a.dy, a.lddy, (int)a.M, a.w, a.dx, a.lddx, pl.shares > 1 ? a.part : nullptr, (int)pl.per};
+    const dim3 grid((unsigned)((a.w.K + 16 * pl.cw - 1) / (16 * pl.cw)), (unsigned)pl.shares);
+    if (a.M <= 16) hipLaunchKernelGGL((w4_bwd_kernel<T, 16, 1>), grid, dim3(256), 0, st, p);
+    else if (a.M <= 32) hipLaunchKernelGGL((w4_bwd_kernel<T, 16, 2>), grid, dim3(256), 0, st, p);
+    else hipLaunchKernelGGL((w4_bwd_kernel<T, 8, 4>), grid, dim3(256), 0, st, p);
+    return hipGetLastError();
 }
 
-hipError_t launch_gemv_w4_bwd(const W4BwdArgs& a, hipStream_t st) {
+template <int T>
+hipError_t run_bwd_gemm(const W4BwdArgs& a, const BwdPlan& pl, hipStream_t st) {
     W4GemmParams p{};
     p.x = a.dy; p.ldx = a.lddy; p.M = a.M; p.R = a.w.N; p.C = a.w.K; p.w = a.w;
     p.y = a.dx; p.ldy = a.lddx; p.part = a.part;
-    const int64_t splits = bwd_splits(a.M, a.w.N, a.w.K);
-    if (splits <= 1)
-        return a.dtype == kFp16 ? pick<kFp16, true, kW4Store>(p, 1, st) : pick<kBf16, true, kW4Store>(p, 1, st);
-    const hipError_t e = a.dtype == kFp16 ? pick<kFp16, true, kW4Part>(p, splits, st)
-                                          : pick<kBf16, true, kW4Part>(p, splits, st);
-    if (e != hipSuccess) return e;
-    const int64_t nsteps = (p.R + 63) / 64, per = (nsteps + splits - 1) / splits;
-    const int real = (int)((nsteps + per - 1) / per);
+    return pl.shares > 1 ? pick<T, true, kW4Part>(p, pl.shares, st) : pick<T, true, kW4Store>(p, 1, st);
+}
+
+template <int T>
+hipError_t bwd(const W4BwdArgs& a, hipStream_t st) {
+    const BwdPlan pl = bwd_plan(a.M, a.w.N, a.w.K);
+    const hipError_t e = pl.cw ? run_bwd<T>(a, pl, st) : run_bwd_gemm<T>(a, pl, st);
+    if (e != hipSuccess || pl.shares == 1) return e;
     const dim3 grid((unsigned)((a.M * (a.w.K / 4) + 255) / 256));
-    if (a.dtype == kFp16)
-        hipLaunchKernelGGL(w4_reduce_kernel<kFp16>, grid, dim3(256), 0, st, a.part, a.M, a.w.K, real, a.dx, a.lddx);
-    else
-        hipLaunchKernelGGL(w4_reduce_kernel<kBf16>, grid, dim3(256), 0, st, a.part, a.M, a.w.K, real, a.dx, a.lddx);
+    hipLaunchKernelGGL(w4_reduce_kernel<T>, grid, dim3(256), 0, st, a.part, a.M, a.w.K, (int)pl.shares, a.dx, a.lddx);
     return hipGetLastError();
+}
+
+}  // namespace
+
+size_t w4_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    const BwdPlan pl = bwd_plan(M, N, K);
+    return pl.shares > 1 ? (size_t)(pl.shares * M * K) * 4 : 0;
+}
+
+hipError_t launch_gemv_w4_bwd(const W4BwdArgs& a, hipStream_t st) {
+    return a.dtype == kFp16 ? bwd<kFp16>(a, st) : bwd<kBf16>(a, st);
 }
 
 hipError_t launch_gate_bwd(const W4GateBwdArgs& a, hipStream_t st) {
