@@ -172,8 +172,13 @@ hipError_t bwd(const W4BwdArgs& a, hipStream_t st) {
     const BwdPlan pl = bwd_plan(a.M, a.w.N, a.w.K);
     const hipError_t e = pl.cw ? run_bwd<T>(a, pl, st) : run_bwd_gemm<T>(a, pl, st);
     if (e != hipSuccess || pl.shares == 1) return e;
-    const dim3 grid((unsigned)((a.M * (a.w.K / 4) + 255) / 256));
-    hipLaunchKernelGGL(w4_reduce_kernel<T>, grid, dim3(256), 0, st, a.part, a.M, a.w.K, (int)pl.shares, a.dx, a.lddx);
+    const int64_t outputs = a.M * a.w.K;
+    if (outputs >= 4 * 256 * 512)
+        hipLaunchKernelGGL((w4_reduce_kernel<T, 4>), dim3((unsigned)((outputs / 4 + 255) / 256)), dim3(256), 0, st,
+                           a.part, a.M, a.w.K, (int)pl.shares, a.dx, a.lddx);
+    else
+        hipLaunchKernelGGL((w4_reduce_kernel<T, 1>), dim3((unsigned)((outputs + 255) / 256)), dim3(256), 0, st, a.part,
+                           a.M, a.w.K, (int)pl.shares, a.dx, a.lddx);
     return hipGetLastError();
 }
 

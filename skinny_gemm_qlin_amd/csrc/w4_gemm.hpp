@@ -396,18 +396,28 @@ __global__ __launch_bounds__(64 * WGM * WGN, 2) void w4_gemm_kernel(const W4Gemm
         }
 }
 
-// out[m,c] = sum over splits of part[s][m][c], in split order
-template <int T>
+// out[m,c] = sum over splits of part[s][m][c], in split order; V columns a thread (4, or 1 where that leaves too
+// few threads), eight splits' loads in flight at once
+template <int T, int V>
 __global__ __launch_bounds__(256) void w4_reduce_kernel(const float* part, int64_t M, int64_t C, int splits,
                                                         uint16_t* y, int64_t ldy) {
-    const int64_t c4 = C / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // C % 32 == 0
-    if (i >= M * c4) return;
-    const int64_t m = i / c4, c = (i - m * c4) * 4;
+    typedef float vec_t __attribute__((ext_vector_type(V)));
+    const int64_t cv = C / V, i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // C % 32 == 0
+    if (i >= M * cv) return;
+    const int64_t m = i / cv, c = (i - m * cv) * V;
     const float* src = part + m * C + c;
-    f32x4v_t v = *(const f32x4v_t*)src;
-    for (int s = 1; s < splits; ++s) v += *(const f32x4v_t*)(src + (int64_t)s * M * C);
+    vec_t sum = {};
+    for (int s = 0; s < splits; s += 8) {
+        vec_t v[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) y[m * ldy + c + e] = f32_to_h<T>(v[e]);
+        for (int e = 0; e < 8; ++e)
+            v[e] = __builtin_nontemporal_load((const vec_t*)(src + (int64_t)(s + e < splits ? s + e : s) * M * C));
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (s + e < splits) sum += v[e];
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) y[m * ldy + c + e] = f32_to_h<T>(sum[e]);
 }
 
 // dgu = [dy u act'(g), dy act(g)], V columns a thread
