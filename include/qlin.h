@@ -365,9 +365,11 @@ int qlin_moe_ffn_mxfp4(const void* x, int64_t ldx, int64_t M, int64_t H,
  * The weight matrix of these calls, N rows of K (group G, g = k / G):
  *   W[n,k] = ws[n,g] * (code[n,k] - zero[n,g])
  *   w   uint8 [N, ldw]   codes 0..15, element 2i in the LOW nibble of byte i;
- *                        pitch ldw in bytes, ldw >= K/2, ldw % 16 == 0
+ *                        pitch ldw in bytes, K/2 <= ldw <= 2^20, ldw % 16 == 0
  *   ws  16-bit [N, K/G]  scales in the activations' type (row-major, dense)
  *   wz  uint8 [N, K/G]   zero points 0..15, or NULL: 8 everywhere
+ * (ws and wz are read in whole aligned 16-byte lines: up to 15 bytes of the
+ * line that an end of the array lies in may be read besides.)
  * dtype is the type of every 16-bit operand and result of the call.
  * Requires K % 32 == 0, 32 <= K <= 2^20, G >= 32, G % 32 == 0, K % G == 0,
  * 1 <= N <= 2^20, 1 <= M <= QLIN_MAX_M_PREFILL.  All sums are fp32.  The
@@ -384,7 +386,8 @@ enum {
 /* y[m,n] = r16( sum_k x[m,k] * W[n,k] + bias[n] ), one rounding.
  *   x 16-bit [M, ldx] (16-byte aligned, ldx % 8 == 0); bias 16-bit [N] or
  *   NULL; y 16-bit [M, ldy].
- * A weight is rounded once to dtype before it is multiplied. */
+ * Up to 16 tokens the scales multiply fp32 sums of code * x (nothing else
+ * rounds); above, a weight is rounded once to dtype before it is multiplied. */
 int qlin_gemv_w4(const void* x, int64_t ldx, int64_t M, int64_t K, int dtype,
                  const uint8_t* w, int64_t ldw, int64_t N, const void* ws, const uint8_t* wz, int64_t group,
                  const void* bias, void* y, int64_t ldy, void* stream);

@@ -13,7 +13,8 @@ inline bool misaligned(const void* p, uintptr_t a) { return ((uintptr_t)p) % a !
 
 inline int launch_status(hipError_t e) { return e == hipSuccess ? QLIN_OK : QLIN_ERR_LAUNCH; }
 
-constexpr int64_t kMaxDim = 1 << 20;  // N (rows of W) and K: indexes of scale groups stay in 32 bits
+constexpr int64_t kMaxDim = 1 << 20;    // N (rows of W) and K: indexes of scale groups stay in 32 bits
+constexpr int64_t kMaxPitch = 1 << 20;  // bytes of a code row: a workgroup has fewer than 4096 rows, offsets in them fit 32 bits
 
 inline bool bad_flag(int dtype) { return dtype != QLIN_DT_BF16 && dtype != QLIN_DT_FP16; }
 
@@ -40,7 +41,7 @@ int qlin_gemv_w4(const void* x, int64_t ldx, int64_t M, int64_t K, int dtype,
     if (!x || !w || !ws || !y) return QLIN_ERR_NULL;
     const int rc = check_shape(M, N, K, group);
     if (rc != QLIN_OK) return rc;
-    if (ldx < K || ldw < K / 2 || ldy < N) return QLIN_ERR_STRIDE;
+    if (ldx < K || ldw < K / 2 || ldw > kMaxPitch || ldy < N) return QLIN_ERR_STRIDE;
     if (misaligned(x, 16) || ldx % 8 != 0 || weight_misaligned(w, ldw, ws) || misaligned(y, 2) ||
         (bias && misaligned(bias, 2)))
         return QLIN_ERR_ALIGN;
@@ -62,7 +63,7 @@ int qlin_gemv_w4_bwd(const void* dy, int64_t lddy, int64_t M, int64_t N, int dty
     if (!dy || !w || !ws || !dx) return QLIN_ERR_NULL;
     const int rc = check_shape(M, N, K, group);
     if (rc != QLIN_OK) return rc;
-    if (lddy < N || ldw < K / 2 || lddx < K) return QLIN_ERR_STRIDE;
+    if (lddy < N || ldw < K / 2 || ldw > kMaxPitch || lddx < K) return QLIN_ERR_STRIDE;
     if (misaligned(dy, 16) || lddy % 8 != 0 || weight_misaligned(w, ldw, ws) || misaligned(dx, 2))
         return QLIN_ERR_ALIGN;
     const size_t need = qlin::w4_bwd_workspace_bytes(M, N, K);
@@ -81,7 +82,7 @@ int qlin_glu_w4(const void* x, int64_t ldx, int64_t M, int64_t K, int dtype,
     if (I < 1 || I > kMaxDim / 2) return QLIN_ERR_SHAPE;
     const int rc = check_shape(M, 2 * I, K, group);
     if (rc != QLIN_OK) return rc;
-    if (ldx < K || ldw < K / 2 || ldy < I || (gu && ldgu < 2 * I)) return QLIN_ERR_STRIDE;
+    if (ldx < K || ldw < K / 2 || ldw > kMaxPitch || ldy < I || (gu && ldgu < 2 * I)) return QLIN_ERR_STRIDE;
     if (misaligned(x, 16) || ldx % 8 != 0 || weight_misaligned(w13, ldw, s13) || misaligned(y, 2) ||
         (gu && misaligned(gu, 2)))
         return QLIN_ERR_ALIGN;
@@ -100,7 +101,7 @@ int qlin_glu_w4_bwd(const void* dy, int64_t lddy, int64_t M, int64_t I, int dtyp
     if (I < 1 || I > kMaxDim / 2) return QLIN_ERR_SHAPE;
     const int rc = check_shape(M, 2 * I, K, group);
     if (rc != QLIN_OK) return rc;
-    if (lddy < I || (gu ? ldgu < 2 * I : ldx < K) || ldw < K / 2 || lddgu < 2 * I || (dx && lddx < K))
+    if (lddy < I || (gu ? ldgu < 2 * I : ldx < K) || ldw < K / 2 || ldw > kMaxPitch || lddgu < 2 * I || (dx && lddx < K))
         return QLIN_ERR_STRIDE;
     if (misaligned(dy, 2) || (gu ? misaligned(gu, 2) : misaligned(x, 16) || ldx % 8 != 0) ||
         weight_misaligned(w13, ldw, s13) || misaligned(dgu, 16) || lddgu % 8 != 0 || (dx && misaligned(dx, 2)))

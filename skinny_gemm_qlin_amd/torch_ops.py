@@ -13,6 +13,9 @@ fallback.
 
     import skinny_gemm_qlin_amd.torch_ops  # registers torch.ops.qlin.*
     y = torch.ops.qlin.gemv_fp8(x, w, ws)
+
+The 4-bit weight operators ``gemv_w4`` and ``glu_w4`` are differentiable in x:
+the weight is frozen (codes, scales, zero points and bias have no gradient).
 """
 from __future__ import annotations
 
@@ -22,7 +25,8 @@ from typing import Optional, Tuple
 import torch
 
 from . import (qlin_act_quant_fp8, qlin_act_quant_i8, qlin_gemv_fp8, qlin_gemv_fp8_blk, qlin_gemv_fp8_blk_ex,
-               qlin_gemv_fp8_w8a8, qlin_gemv_i8, qlin_linear_i8, qlin_moe_ffn_mxfp4, qlin_moe_mxfp4)
+               qlin_gemv_fp8_w8a8, qlin_gemv_i8, qlin_gemv_w4, qlin_gemv_w4_bwd, qlin_glu_w4, qlin_glu_w4_bwd,
+               qlin_linear_i8, qlin_moe_ffn_mxfp4, qlin_moe_mxfp4)
 
 hits = collections.Counter()
 
@@ -174,3 +178,116 @@ def _(x, wr, w13, s13, w2, s2, topk, alpha=1.0, limit=10.0):
     M, H = x.shape
     return (x.new_empty((M, H), dtype=torch.bfloat16), x.new_empty((M, topk), dtype=torch.int32),
             x.new_empty((M, topk), dtype=torch.float32))
+
+
+# ----------------------------------------------------------------------------- 4-bit weights with group scales
+
+def _rows8(t: torch.Tensor) -> torch.Tensor:
+    """A gradient as the kernels read it: rows of unit stride, 16-byte aligned, a pitch that is a multiple
+    of 8.  Autograd also hands out expanded and transposed gradients; those are copied."""
+    rows, cols = t.shape
+    if t.stride(1) == 1 and t.data_ptr() % 16 == 0 and (rows == 1 or (t.stride(0) % 8 == 0 and t.stride(0) >= cols)):
+        return t
+    out = t.new_empty((rows, (cols + 7) // 8 * 8))[:, :cols]
+    out.copy_(t)
+    return out
+
+
+def _frozen(name: str, needs) -> None:
+    if any(needs):
+        raise RuntimeError(f"{name}: the 4-bit weight is frozen, only x has a gradient")
+
+
+@torch.library.custom_op("qlin::gemv_w4", mutates_args=())
+def gemv_w4(x: torch.Tensor, w: torch.Tensor, ws: torch.Tensor, wz: Optional[torch.Tensor] = None,
+            bias: Optional[torch.Tensor] = None) -> torch.Tensor:
+    hits["gemv_w4"] += 1
+    return qlin_gemv_w4(x, w, ws, wz, bias=bias)
+
+
+@gemv_w4.register_fake
+def _(x, w, ws, wz=None, bias=None):
+    return x.new_empty((x.shape[0], w.shape[0]))
+
+
+@torch.library.custom_op("qlin::gemv_w4_bwd", mutates_args=())
+def gemv_w4_bwd(dy: torch.Tensor, w: torch.Tensor, ws: torch.Tensor, wz: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Input gradient dx [M, K] of gemv_w4 from dy [M, N] in any layout."""
+    hits["gemv_w4_bwd"] += 1
+    return qlin_gemv_w4_bwd(_rows8(dy), w, ws, wz)
+
+
+@gemv_w4_bwd.register_fake
+def _(dy, w, ws, wz=None):
+    return dy.new_empty((dy.shape[0], 2 * w.shape[1]))
+
+
+def _gemv_w4_setup(ctx, inputs, output):
+    _, w, ws, wz, _ = inputs
+    _frozen("gemv_w4", ctx.needs_input_grad[1:])
+    ctx.save_for_backward(w, ws, wz)
+
+
+def _gemv_w4_grad(ctx, dy):
+    w, ws, wz = ctx.saved_tensors
+    return torch.ops.qlin.gemv_w4_bwd(dy, w, ws, wz), None, None, None, None
+
+
+gemv_w4.register_autograd(_gemv_w4_grad, setup_context=_gemv_w4_setup)
+
+
+@torch.library.custom_op("qlin::glu_w4", mutates_args=())
+def glu_w4(x: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor, z13: Optional[torch.Tensor] = None, act: int = 0,
+           keep: bool = False) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Gated feed-forward front -> (y [M, I], gu).  keep: gu [M, 2I] holds gate and up
+    for the backward pass; otherwise gu is empty and they are recomputed from x."""
+    hits["glu_w4"] += 1
+    gu = x.new_empty((x.shape[0], (w13.shape[0] + 7) // 8 * 8))[:, :w13.shape[0]] if keep else None
+    y = qlin_glu_w4(x, w13, s13, z13, act=act, gu=gu)
+    return y, x.new_empty((0, 0)) if gu is None else gu
+
+
+@glu_w4.register_fake
+def _(x, w13, s13, z13=None, act=0, keep=False):
+    n = w13.shape[0]
+    gu = x.new_empty((x.shape[0], (n + 7) // 8 * 8))[:, :n] if keep else x.new_empty((0, 0))
+    return x.new_empty((x.shape[0], n // 2)), gu
+
+
+@torch.library.custom_op("qlin::glu_w4_bwd", mutates_args=())
+def glu_w4_bwd(dy: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor, z13: Optional[torch.Tensor] = None,
+               x: Optional[torch.Tensor] = None, gu: Optional[torch.Tensor] = None,
+               act: int = 0) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(dx [M, K], dgu [M, 2I]) of glu_w4 from dy [M, I] in any layout and gu or x."""
+    hits["glu_w4_bwd"] += 1
+    return qlin_glu_w4_bwd(_rows8(dy), w13, s13, z13, act=act, x=x, gu=gu)
+
+
+@glu_w4_bwd.register_fake
+def _(dy, w13, s13, z13=None, x=None, gu=None, act=0):
+    n = w13.shape[0]
+    return (dy.new_empty((dy.shape[0], 2 * w13.shape[1])),
+            dy.new_empty((dy.shape[0], (n + 7) // 8 * 8))[:, :n])
+
+
+def _glu_w4_setup(ctx, inputs, output):
+    x, w13, s13, z13, act, keep = inputs
+    _frozen("glu_w4", ctx.needs_input_grad[1:])
+    ctx.set_materialize_grads(False)
+    ctx.act = act
+    ctx.keep = keep
+    ctx.save_for_backward(output[1] if keep else x, w13, s13, z13)
+
+
+def _glu_w4_grad(ctx, dy, dgu):
+    kept, w13, s13, z13 = ctx.saved_tensors
+    if dgu is not None:
+        raise RuntimeError("glu_w4: gu is kept for the backward pass and has no gradient of its own")
+    if dy is None:
+        return None, None, None, None, None, None
+    x, gu = (None, kept) if ctx.keep else (kept, None)
+    dx, _ = torch.ops.qlin.glu_w4_bwd(dy, w13, s13, z13, x, gu, ctx.act)
+    return dx, None, None, None, None, None
+
+
+glu_w4.register_autograd(_glu_w4_grad, setup_context=_glu_w4_setup)

@@ -26,7 +26,7 @@ SHAPES = [({"M": 0}, -2), ({"M": 16385}, -2), ({"N": 0}, -2), ({"N": (1 << 20) +
           ({"K": 48, "ldw": 64, "group": 16}, -2), ({"K": (1 << 20) + 32}, -2), ({"group": 0}, -2),
           ({"group": 16}, -2), ({"group": 96}, -2), ({"group": -32}, -2), ({"group": 2048}, -2),
           ({"dtype": 2}, -6), ({"dtype": -1}, -6), ({"w": None}, -1), ({"ws": None}, -1),
-          ({"ldw": 496}, -3), ({"ldw": 520}, -4), ({"w": A + 8}, -4), ({"ws": A + 1}, -4)]
+          ({"ldw": 496}, -3), ({"ldw": (1 << 20) + 16}, -3), ({"ldw": 520}, -4), ({"w": A + 8}, -4), ({"ws": A + 1}, -4)]
 
 
 def _with(defaults, changes):
@@ -60,7 +60,8 @@ def test_gemv_w4_bwd_refusals(q, change, status):
     if "N" in change:
         a["lddy"] = 1 << 21
     if "K" in change:
-        a["lddx"] = a["ldw"] = 1 << 21
+        a["lddx"] = 1 << 21
+        a["ldw"] = 1 << 20
     assert q.qlin_gemv_w4_bwd(a["dy"], a["lddy"], a["M"], a["N"], a["dtype"], a["w"], a["ldw"], a["K"], a["ws"],
                               a["wz"], a["group"], a["dx"], a["lddx"], a["work"], a["size"], None) == status
 
@@ -79,7 +80,8 @@ def test_glu_w4_refusals(q, change, status):
     a = _with(dict(x=A, ldx=1024, M=1, K=1024, dtype=1, w=A, ldw=512, N=64, ws=A, wz=None, group=128, act=0, y=A,
                    ldy=64, gu=None, ldgu=64), change)
     if "K" in change:
-        a["ldx"] = a["ldw"] = 1 << 21
+        a["ldx"] = 1 << 21
+        a["ldw"] = 1 << 20
     if "N" in change:
         a["ldy"] = a["ldgu"] = 1 << 22
     assert q.qlin_glu_w4(a["x"], a["ldx"], a["M"], a["K"], a["dtype"], a["w"], a["ldw"], a["N"] // 2, a["ws"],
@@ -95,7 +97,8 @@ def test_glu_w4_bwd_refusals(q, change, status):
     a = _with(dict(dy=A, lddy=64, M=1, N=64, dtype=0, act=0, x=A, ldx=1024, gu=A, ldgu=64, w=A, ldw=512, K=1024, ws=A,
                    wz=A, group=128, dgu=A, lddgu=64, dx=A, lddx=1024, work=A, size=1 << 40), change)
     if "K" in change:
-        a["ldx"] = a["lddx"] = a["ldw"] = 1 << 21
+        a["ldx"] = a["lddx"] = 1 << 21
+        a["ldw"] = 1 << 20
     if "N" in change:
         a["lddy"] = a["ldgu"] = a["lddgu"] = 1 << 22
     assert q.qlin_glu_w4_bwd(a["dy"], a["lddy"], a["M"], a["N"] // 2, a["dtype"], a["act"], a["x"], a["ldx"], a["gu"],
@@ -160,3 +163,41 @@ def test_gradient_formula_against_differences(kind):
         e[m, k] = h
         num = (loss((x + e) @ W.T) - loss((x - e) @ W.T)) / (2 * h)
         assert abs(num - dx[m, k]) < 1e-5 * (1 + abs(dx[m, k]))
+
+
+# ----------------------------------------------------------------------------- the binding's own refusals (before any launch)
+
+def test_binding_refusals():
+    import skinny_gemm_qlin_amd as ql
+    x = torch.zeros((2, 64), dtype=torch.bfloat16)
+    w = torch.zeros((8, 32), dtype=torch.uint8)
+    ws = torch.zeros((8, 2), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="device"):
+        ql.qlin_gemv_w4(x, w, ws)                                    # host tensors
+    for bad in (x.float(), x.to(torch.int16)):
+        with pytest.raises(TypeError):
+            ql.qlin_gemv_w4(bad, w, ws)
+    for name, args in [("w", (x, w.to(torch.int8), ws)), ("ws", (x, w, ws.half()))]:
+        with pytest.raises((TypeError, ValueError)):
+            ql.qlin_gemv_w4(*args)
+        with pytest.raises((TypeError, ValueError)):
+            ql.qlin_glu_w4(*args)
+        with pytest.raises((TypeError, ValueError)):
+            ql.qlin_gemv_w4_bwd(*args)
+        with pytest.raises((TypeError, ValueError)):
+            ql.qlin_glu_w4_bwd(*args, gu=args[0])
+
+
+def test_fake_shapes():
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    import skinny_gemm_qlin_amd.torch_ops  # noqa: F401
+    with FakeTensorMode():
+        x = torch.empty((5, 64), dtype=torch.float16)
+        w, s, z = torch.empty((10, 32), dtype=torch.uint8), torch.empty((10, 2), dtype=torch.float16), None
+        assert torch.ops.qlin.gemv_w4(x, w, s, z).shape == (5, 10)
+        y, gu = torch.ops.qlin.glu_w4(x, w, s, z, 1, True)
+        assert y.shape == (5, 5) and gu.shape == (5, 10) and gu.stride() == (16, 1) and y.dtype == torch.float16
+        assert torch.ops.qlin.glu_w4(x, w, s, z)[1].shape == (0, 0)
+        assert torch.ops.qlin.gemv_w4_bwd(gu, w, s, z).shape == (5, 64)
+        dx, dgu = torch.ops.qlin.glu_w4_bwd(y, w, s, z, x, None, 0)
+        assert dx.shape == (5, 64) and dgu.shape == (5, 10)
