@@ -17,16 +17,9 @@ HALF_STEP = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11}  # largest relative rounding
 
 def dense(w, ws, wz, group):
     """float64 [N, K] from codes uint8 [N, K/2], ws [N, K/G], wz [N, K/G] or None."""
-    N, kh = w.shape
-    K = 2 * kh
-    W = np.empty((N, K))
-    for n in range(N):
-        for g in range(K // group):
-            z = 8.0 if wz is None else float(wz[n, g])
-            b = w[n, g * group // 2:(g + 1) * group // 2]
-            W[n, g * group:(g + 1) * group:2] = ws[n, g] * ((b & 15).astype(np.float64) - z)
-            W[n, g * group + 1:(g + 1) * group:2] = ws[n, g] * ((b >> 4).astype(np.float64) - z)
-    return W
+    codes = np.stack([w & 15, w >> 4], axis=2).reshape(len(w), -1).astype(np.float64)
+    zero = 8.0 if wz is None else np.repeat(wz.astype(np.float64), group, axis=1)
+    return np.repeat(ws, group, axis=1) * (codes - zero)
 
 
 def dense_parts(w, ws, wz, group):

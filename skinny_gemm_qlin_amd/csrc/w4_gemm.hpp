@@ -112,7 +112,6 @@ __global__ __launch_bounds__(64 * WGM * WGN, 2) void w4_gemm_kernel(const W4Gemm
     // forward: the scales of 4 groups at a time
     const uint16_t* srow = nullptr;
     const uint8_t* zrow = nullptr;
-    const bool wide = p.w.N * ngroups >= 4;
     int left = 0;  // scales from the row's first to the matrix's last
     // backward: the columns are fixed
     const uint16_t* ssrc = nullptr;
@@ -178,20 +177,14 @@ __global__ __launch_bounds__(64 * WGM * WGN, 2) void w4_gemm_kernel(const W4Gemm
         }
     };
     // forward: scales and zeros of groups 4v .. 4v + 3 of the run's row, as one load each.  The four may reach into
-    // the next row; at the end of the matrix they are its last four, and with fewer than four in all the first ones.
+    // the next row; at the end of the matrix they are its last four (there are four: the launcher sees to it).
     struct Window { uint2 s; uint32_t z; };
-    auto window_first = [&](int v) { return wide ? (v * 4 < left - 4 ? v * 4 : left - 4) : 0; };
+    auto window_first = [&](int v) { return v * 4 < left - 4 ? v * 4 : left - 4; };
     auto load_window = [&](int v) {
         Window w;
         const int first = window_first(v);
-        if (wide) {
-            __builtin_memcpy(&w.s, srow + first, 8);
-            __builtin_memcpy(&w.z, zrow + first, 4);
-        } else {
-            const int b1 = left > 1 ? 1 : 0, b2 = left > 2 ? 2 : 0;
-            w.s = make_uint2((uint32_t)srow[0] | (uint32_t)srow[b1] << 16, srow[b2]);
-            w.z = (uint32_t)zrow[0] | (uint32_t)zrow[b1] << 8 | (uint32_t)zrow[b2] << 16;
-        }
+        __builtin_memcpy(&w.s, srow + first, 8);
+        __builtin_memcpy(&w.z, zrow + first, 4);
         return w;
     };
     auto group_of = [&](int64_t unit) {  // group of the 32 elements from 32 * unit; uniform
