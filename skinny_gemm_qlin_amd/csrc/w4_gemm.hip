@@ -16,9 +16,11 @@ uint32_t ratio_magic(int64_t group, int unit) {
 }
 
 template <int T, bool BWD, int EPI, int BM, int BN, int WGM, int WGN>
-hipError_t run(W4GemmParams p, int64_t splits, hipStream_t st) {
+hipError_t run(W4GemmParams p, int64_t c_first, int64_t c_count, int64_t splits, hipStream_t st) {
     constexpr int CT = EPI == kW4Glu || EPI == kW4GluBwd ? BN / 2 : BN;
-    const int64_t tiles = ((p.M + BM - 1) / BM) * ((p.C + CT - 1) / CT);
+    const int64_t tiles = ((p.M + BM - 1) / BM) * ((c_count + CT - 1) / CT);
+    p.c_first = c_first;
+    p.c_count = c_count;
     const int64_t nsteps = (p.R + 63) / 64;
     p.steps = (nsteps + splits - 1) / splits;
     p.ratio_magic = ratio_magic(p.w.group, 32);
@@ -31,24 +33,45 @@ hipError_t run(W4GemmParams p, int64_t splits, hipStream_t st) {
 // compute unit), of a 128 x 128 tile 1.05 us alone on its unit and 1.2 to 1.4 us where two share one (2048 tokens,
 // 17408 x 5120, 80 steps: 544 large tiles 478 us, 2176 small ones 489 us; 509 tokens, 4096 x 7168, 112 steps: 32
 // large ones 203 us, 128 small ones 120 us; 256 tokens, 17408 x 5120, 272 small ones 120 us).
-float gemm_us(int64_t M, int64_t cols, int64_t R, int tile) {
-    const int64_t tiles = ((M + tile - 1) / tile) * ((cols + tile - 1) / tile), steps = (R + 63) / 64;
-    if (tile == 256) return 10.f + (float)((tiles + 255) / 256 * steps) * 1.95f;
+float large_us(int64_t tiles, int64_t steps) { return (float)((tiles + 255) / 256 * steps) * 1.95f; }
+
+float small_us(int64_t tiles, int64_t steps) {
     const int64_t full = tiles / 512, rest = tiles - full * 512;
-    return 10.f + (float)steps * ((float)full * 1.22f + (rest == 0 ? 0.f : (rest <= 256 ? 1.05f : 1.4f)));
+    return (float)steps * ((float)full * 1.22f + (rest == 0 ? 0.f : (rest <= 256 ? 1.05f : 1.4f)));
 }
 
-template <int T, bool BWD, int EPI>
-hipError_t pick(const W4GemmParams& p, int64_t splits, hipStream_t st) {
-    const int64_t cols = (EPI == kW4Glu || EPI == kW4GluBwd ? 2 : 1) * p.C;
-    if (BWD ? p.M <= 512 : gemm_us(p.M, cols, p.R, 128) < gemm_us(p.M, cols, p.R, 256))
-        return run<T, BWD, EPI, 128, 128, 2, 2>(p, splits, st);
-    return run<T, BWD, EPI, 256, 256, 2, 4>(p, splits, st);
+// Forward: `large` tile columns of 256 in large tiles, the rest in small ones.  Large tiles that would leave the
+// last of several rounds of workgroups part empty give their last columns to small tiles (2048 tokens: 17408 x 5120,
+// 2.1 rounds, 475 us in large tiles, 429 us so; 28672 x 4096 gated, 3.5 rounds, 532 and 521 us).
+struct GemmPlan { int64_t large; float us; };
+
+GemmPlan gemm_plan(int64_t M, int64_t cols, int64_t R) {
+    const int64_t steps = (R + 63) / 64, tm = (M + 255) / 256, tc = (cols + 255) / 256, tm2 = (M + 127) / 128;
+    GemmPlan o{0, 10.f + small_us(tm2 * ((cols + 127) / 128), steps)};
+    const float all = 10.f + large_us(tm * tc, steps);
+    if (all <= o.us) o = {tc, all};
+    const int64_t part = (tm * tc - 1) / 256 * 256 / tm;  // tile columns of all rounds but the last
+    if (part > 0) {
+        const float both = 15.f + large_us(tm * part, steps) + small_us(tm2 * ((cols - part * 256 + 127) / 128), steps);
+        if (both < o.us) o = {part, both};
+    }
+    return o;
+}
+
+template <int T, int EPI>
+hipError_t forward(const W4GemmParams& p, hipStream_t st) {
+    constexpr int fold = EPI == kW4Store ? 1 : 2;  // rows of W a column of the output takes
+    const int64_t large = gemm_plan(p.M, fold * p.C, p.R).large * 256 / fold, first = large < p.C ? large : p.C;
+    if (first > 0) {
+        const hipError_t e = run<T, false, EPI, 256, 256, 2, 4>(p, 0, first, 1, st);
+        if (e != hipSuccess) return e;
+    }
+    return first == p.C ? hipSuccess : run<T, false, EPI, 128, 128, 2, 2>(p, first, p.C - first, 1, st);
 }
 
 template <int EPI>
-hipError_t pick_dtype(int dtype, const W4GemmParams& p, hipStream_t st) {
-    return dtype == kFp16 ? pick<kFp16, false, EPI>(p, 1, st) : pick<kBf16, false, EPI>(p, 1, st);
+hipError_t gemm(int dtype, const W4GemmParams& p, hipStream_t st) {
+    return dtype == kFp16 ? forward<kFp16, EPI>(p, st) : forward<kBf16, EPI>(p, st);
 }
 
 hipError_t run_few(int dtype, W4FewParams p, const W4FewPlan& pl, hipStream_t st) {
@@ -63,7 +86,7 @@ hipError_t run_few(int dtype, W4FewParams p, const W4FewPlan& pl, hipStream_t st
 // compute units idle (128 tokens, 4096 x 7168: 22 us against 102), and matrices of fewer than four scales, which
 // the GEMM loads four at a time.
 bool use_mid(int64_t M, const W4Weight& w, const W4MidPlan& pl) {
-    return w.N * (w.K / w.group) < 4 || pl.us < fminf(gemm_us(M, w.N, w.K, 128), gemm_us(M, w.N, w.K, 256));
+    return w.N * (w.K / w.group) < 4 || pl.us < gemm_plan(M, w.N, w.K).us;
 }
 
 hipError_t run_mid(int dtype, W4MidParams p, const W4MidPlan& pl, hipStream_t st) {
@@ -92,7 +115,7 @@ hipError_t launch_gemv_w4(const W4LinearArgs& a, hipStream_t st) {
     W4GemmParams p{};
     p.x = a.x; p.ldx = a.ldx; p.M = a.M; p.R = a.w.K; p.C = a.w.N; p.w = a.w;
     p.bias = a.bias; p.y = a.y; p.ldy = a.ldy;
-    return pick_dtype<kW4Store>(a.dtype, p, st);
+    return gemm<kW4Store>(a.dtype, p, st);
 }
 
 hipError_t launch_glu_w4(const W4GluArgs& a, hipStream_t st) {
@@ -113,7 +136,7 @@ hipError_t launch_glu_w4(const W4GluArgs& a, hipStream_t st) {
     W4GemmParams p{};
     p.x = a.x; p.ldx = a.ldx; p.M = a.M; p.R = a.w.K; p.C = a.I; p.w = a.w; p.I = a.I;
     p.y = a.y; p.ldy = a.ldy; p.gu = a.gu; p.ldgu = a.ldgu; p.dy = a.dy; p.lddy = a.lddy; p.act = a.act;
-    return a.dy ? pick_dtype<kW4GluBwd>(a.dtype, p, st) : pick_dtype<kW4Glu>(a.dtype, p, st);
+    return a.dy ? gemm<kW4GluBwd>(a.dtype, p, st) : gemm<kW4Glu>(a.dtype, p, st);
 }
 
 // How the input gradient is laid out: shares of the reduction over N, so that short batches and narrow outputs
@@ -164,7 +187,11 @@ hipError_t run_bwd_gemm(const W4BwdArgs& a, const BwdPlan& pl, hipStream_t st) {
     W4GemmParams p{};
     p.x = a.dy; p.ldx = a.lddy; p.M = a.M; p.R = a.w.N; p.C = a.w.K; p.w = a.w;
     p.y = a.dx; p.ldy = a.lddx; p.part = a.part;
-    return pl.shares > 1 ? pick<T, true, kW4Part>(p, pl.shares, st) : pick<T, true, kW4Store>(p, 1, st);
+    if (a.M <= 512)
+        return pl.shares > 1 ? run<T, true, kW4Part, 128, 128, 2, 2>(p, 0, p.C, pl.shares, st)
+                             : run<T, true, kW4Store, 128, 128, 2, 2>(p, 0, p.C, 1, st);
+    return pl.shares > 1 ? run<T, true, kW4Part, 256, 256, 2, 4>(p, 0, p.C, pl.shares, st)
+                         : run<T, true, kW4Store, 256, 256, 2, 4>(p, 0, p.C, 1, st);
 }
 
 template <int T>

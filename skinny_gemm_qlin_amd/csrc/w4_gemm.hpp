@@ -33,6 +33,7 @@ enum W4Epi { kW4Store = 0, kW4Glu = 1, kW4GluBwd = 2, kW4Part = 3 };
 struct W4GemmParams {
     const uint16_t* x; int64_t ldx; int64_t M;  // left operand [M][R]
     int64_t R, C;                               // reduction length, output columns
+    int64_t c_first, c_count;                   // of which this launch computes c_count from c_first
     W4Weight w; int64_t I;                      // gated: columns C = I, rows n and I + n
     const uint16_t* bias; uint16_t* y; int64_t ldy;
     uint16_t* gu; int64_t ldgu; const uint16_t* dy; int64_t lddy; int act;
@@ -69,12 +70,12 @@ __global__ __launch_bounds__(64 * WGM * WGN, 2) void w4_gemm_kernel(const W4Gemm
 
     const int64_t M = p.M, R = p.R, C = p.C;
     constexpr int CT = kGlu ? BN / 2 : BN;  // output columns per workgroup
-    const int64_t tiles_m = (M + BM - 1) / BM, tiles_c = (C + CT - 1) / CT, tiles = tiles_m * tiles_c;
+    const int64_t tiles_m = (M + BM - 1) / BM, tiles_c = (p.c_count + CT - 1) / CT, tiles = tiles_m * tiles_c;
     const int64_t t = (int64_t)(blockIdx.x % 8) * (gridDim.x / 8) + blockIdx.x / 8;  // an XCD takes adjacent tiles
     if (t >= tiles) return;  // workgroup-uniform
     const int64_t bsz = kW4BandM * tiles_c, band = t / bsz, rr = t - band * bsz;
     const int64_t gm = tiles_m - band * kW4BandM < kW4BandM ? tiles_m - band * kW4BandM : kW4BandM;
-    const int64_t c0 = (rr / gm) * CT, m0 = (band * kW4BandM + rr % gm) * BM;
+    const int64_t c0 = p.c_first + (rr / gm) * CT, m0 = (band * kW4BandM + rr % gm) * BM;
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
     const int64_t nsteps = (R + BR - 1) / BR;
     const int64_t s0 = (int64_t)blockIdx.y * p.steps, s1 = s0 + p.steps < nsteps ? s0 + p.steps : nsteps;
