@@ -37,14 +37,21 @@
 //   rows of which it walks with D tiles requested ahead.  D is small on
 //   purpose: about 20-32 KB a compute unit in flight.  With all loads requested
 //   at once (17408 x 5120: 9 tiles) the first waves are served first and the
-//   last one unpacks its whole share alone at the end: 13.4 us, D = 3 11.3, D =
-//   1 10.4 us; two or more uneven rounds of workgroups 13-16 us.
+//   last one unpacks its whole share alone at the end (2 us more than D = 1);
+//   two or more uneven rounds of workgroups cost 2 to 5 us.
 //
-// * Token rows, scales and zero points are copied to LDS by the whole workgroup
-//   ahead of the weights (global_load_lds, no registers); the barrier leaves the weight loads outstanding.  The
-//   waves' sums are added in wave order through LDS (deterministic, no
-//   workspace).  Rows longer than 16 waves' lines (K > 8192), or too long for
-//   their tokens' share of LDS, are walked in passes.
+// * Token rows, scales and zero points go to LDS ahead of the weights
+//   (global_load_lds, no registers): the scales by the whole workgroup, one
+//   barrier, which leaves the weight loads outstanding; its own lines of the
+//   token rows by each wave, without a barrier, so that waves walk a long row
+//   independently (with a barrier a pass and all tokens' slice shared: 14336 x
+//   4099, 5 tokens 19.6 us, now 17.4).  The waves' sums are added in wave order
+//   through LDS (deterministic, no workspace).  Rows longer than 16 waves'
+//   lines (K > 8192 or 4096), or too long for LDS, are walked in passes.
+//
+// Measured (bf16, zero points, groups of 128, weights cold): 17408 x 5120, one
+// token 13.1 us (3.6 TB/s of codes and scales), 8 tokens 15.0, 16 tokens 17.9;
+// 28672 x 4096 gated, one token 14.9 us (4.1 TB/s); 1024 x 1024 3.8 us.
 #pragma once
 #include "w4_device.hpp"
 #include "w4_launch.hpp"
@@ -63,23 +70,23 @@ struct W4FewParams {
     uint32_t ratio_magic;             // fold units per group r: unit / r = mulhi(unit, magic), 0: r = 1
 };
 
-// floats that an output's wave sums take: whole 16 bytes, and an odd number of them so that rows start in different banks
-__host__ __device__ inline int w4_few_red(int nw) { return ((nw + 3) / 4 | 1) * 4; }
-constexpr int kW4FewPad = 8;  // elements between staged token rows: 16 bytes, so the rows start in different banks
+// floats that an output's wave sums take: whole 16 bytes, not 16 of them so that rows start in different banks
+__host__ __device__ inline int w4_few_red(int nw) { return nw > 12 ? 20 : (nw + 3) / 4 * 4; }
 
-// Dynamic LDS: the token rows' slice of a pass, X of its fold units, scales and zero points as they are in
+constexpr int kW4FewLoad = 512 + 8;  // elements that a 1 KB load of token rows takes: the next starts 16 bytes of banks on
+
+// Dynamic LDS: each wave's lines of the token rows, X of its fold units, scales and zero points as they are in
 // memory (from the 16-byte line their block starts in), the waves' sums.
 struct W4FewLds { uint32_t xsum, s, z, red, total; };
 
-__host__ __device__ inline W4FewLds w4_few_lds(int M, int U, int PL, int wrows, int groups, int nw) {
-    const uint32_t KP = (uint32_t)(nw * PL * 256);
+__host__ __device__ inline W4FewLds w4_few_lds(int M, int U, int PL, int cols, int wrows, int groups, int nw) {
     auto up = [](uint32_t b) { return (b + 15u) / 16u * 16u; };
     W4FewLds o;
-    o.xsum = (uint32_t)M * (KP + kW4FewPad) * 2;
+    o.xsum = (uint32_t)(nw * ((PL * M + 1) / 2)) * kW4FewLoad * 2;
     o.s = o.xsum + (uint32_t)nw * (PL * (128 / U)) * (M > 8 ? 128 : 64);
     o.z = o.s + up((uint32_t)(wrows * groups * 2)) + 64;  // gated: two blocks, each with its own start and end
     o.red = o.z + up((uint32_t)(wrows * groups)) + 64;
-    o.total = o.red + (uint32_t)(M * wrows * w4_few_red(nw)) * 4;
+    o.total = o.red + (uint32_t)(M * cols * w4_few_red(nw)) * 4;
     return o;
 }
 
@@ -98,13 +105,14 @@ __global__ __launch_bounds__(1024) void w4_few_kernel(const W4FewParams p) {
     const int K = (int)p.w.K;
     const int64_t c0 = (int64_t)blockIdx.x * p.rows;
     const int CT = p.C - c0 < p.rows ? (int)(p.C - c0) : p.rows;  // columns of this workgroup, at least 1
-    const int KP = NW * PL * 256, XP = KP + kW4FewPad, G = p.groups;  // KP: K of a pass
+    const int KP = NW * PL * 256, G = p.groups;  // KP: K of a pass
     const bool glu = p.I > 0;
     const int parts = glu ? 2 : 1, GT = (CT + TR - 1) / TR, TT = parts * GT;  // tiles; gated: gate and up alternate
-    const W4FewLds at = w4_few_lds(M, U, PL, TT * TR, G, NW);
-    uint16_t* xs = (uint16_t*)w4f_lds;                // [M][XP], zero past K
+    const W4FewLds at = w4_few_lds(M, U, PL, parts * CT, TT * TR, G, NW);
+    const int xloads = (PL * M + 1) / 2;                    // of 1 KB: two token lines each
+    uint16_t* xw = (uint16_t*)w4f_lds + wv * xloads * kW4FewLoad;  // this wave's [token][line][256], zero past K
     float* xsum = (float*)(w4f_lds + at.xsum);        // [wave][NU][16]
-    float* red = (float*)(w4f_lds + at.red);          // [token][TT * TR][RS]: the waves' sums
+    float* red = (float*)(w4f_lds + at.red);          // [token][gate and up][CT][RS]: the waves' sums
     const int RS = w4_few_red(NW);
 
     // ---- staging, ahead of the weights (loads return in order) and straight into LDS: 16 bytes a thread
@@ -114,15 +122,23 @@ __global__ __launch_bounds__(1024) void w4_few_kernel(const W4FewParams p) {
                 __builtin_amdgcn_global_load_lds((const void*)((const uint8_t*)src + o + tid * 16),
                                                  (lds_void_t*)((uint8_t*)dst + o + wv * 1024), 16, 0, 0);
     };
-    auto stage_x = [&](int k0) {
-        const int k = k0 + tid * 8;  // the workgroup's threads cover a slice (PL = 2) or twice that (PL = 1)
-        if (PL > 1 || tid * 8 < KP)
-            for (int m = 0; m < M; ++m)
-                __builtin_amdgcn_global_load_lds(
-                    k < K ? (const void*)(p.x + m * p.ldx + k) : (const void*)&kW4Zero16,
-                    (lds_void_t*)(xs + m * XP + wv * 512), 16, 0, 0);
+    // Each wave stages its own lines and so needs no barrier for them.  A load takes 512 bytes twice: a token's two
+    // lines, or two tokens' one.  The 16-byte chunks of a line are permuted so that the A operands' reads (the same
+    // chunk of 16 tokens, or of the two halves of 8) fall into different banks.
+    auto place = [&](int chunk, int sub) {  // its own inverse
+        return chunk ^ (PL > 1 ? (chunk >> 4) * 8 : sub * 8 ^ (chunk >> 4) * 4);
     };
-    stage_x(0);
+    auto stage_x = [&](int k0) {
+        const int sub = lane >> 5, k = k0 + (PL > 1 ? sub * 256 : 0) + place(lane & 31, sub) * 8;
+        const bool in = k < K;
+        const int64_t step = in ? (PL > 1 ? p.ldx : 2 * p.ldx) : 0;
+        const uint16_t* src = in ? p.x + (PL > 1 ? 0 : sub * p.ldx) + k : (const uint16_t*)&kW4Zero16;
+        for (int i = 0; i < xloads; ++i, src += step) {
+            if (PL == 1 && 2 * i + 1 == M && in) src -= sub * p.ldx;  // no token M: the last one again
+            __builtin_amdgcn_global_load_lds((const void*)src, (lds_void_t*)(xw + i * kW4FewLoad), 16, 0, 0);
+        }
+    };
+    stage_x(wv * PL * 256);
     // The scales of adjacent rows are one contiguous block, which may start anywhere: the 16-byte lines that
     // hold it are copied (at most 15 bytes more at each end, of the same line), and read at its offset.
     const bool has_z = p.w.wz != nullptr;
@@ -179,8 +195,25 @@ __global__ __launch_bounds__(1024) void w4_few_kernel(const W4FewParams p) {
     float nx[NC];  // -X of row n of A and that unit
     int gi[NC];    // index of the unit's scale in this lane's row of a tile
 
+    // where this lane's sums go: token token0 + 4r (FULL) or + 2r of register r, column n of a tile
+    const int token0 = FULL ? q : q & 1, red_step = (FULL ? 4 : 2) * parts * CT * RS;
+    float* red_lane = red + (token0 * parts * CT + n) * RS + wv;
+
+    // A tile is waited for, and then the load that follows it into flight is issued before the work on it begins;
+    // left to itself the compiler issues that load before the wait or after the work.
+    u32x4_t now[PL][LH];
+    auto take = [&](int slot) {
+#pragma unroll
+        for (int l = 0; l < PL; ++l)
+#pragma unroll
+            for (int v = 0; v < LH; ++v) {
+                now[l][v] = w[slot][l][v];
+                asm volatile("" : "+v"(now[l][v]));
+            }
+    };
+
     // ---- products, tile by tile as the weights arrive
-    auto tile = [&](int slot, int t, bool add) {
+    auto tile = [&](int t, bool add) {
         const int up = glu ? t & 1 : 0, g0 = (glu ? t >> 1 : t) * TR * G;
         const uint16_t* ss = (const uint16_t*)(w4f_lds + (up ? sat[1] : sat[0])) + g0;
         const uint8_t* zs = w4f_lds + (up ? zat[1] : zat[0]) + g0;
@@ -207,9 +240,9 @@ __global__ __launch_bounds__(1024) void w4_few_kernel(const W4FewParams p) {
                 uint32_t d[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    d[j] = w[slot][l][v][j];
+                    d[j] = now[l][v][j];
                     if constexpr (FULL) {  // half 0: lanes n >= 8 fetch rows 8-15's first half, half 1: n < 8 rows 0-7's second
-                        const int keep = (int)d[j], other = (int)w[slot][l][v ^ (LH - 1)][j];
+                        const int keep = (int)d[j], other = (int)now[l][v ^ (LH - 1)][j];
                         d[j] = (uint32_t)(v == 0 ? __builtin_amdgcn_update_dpp(keep, other, 0x128, 0xF, 0xC, false)
                                                  : __builtin_amdgcn_update_dpp(keep, other, 0x128, 0xF, 0x3, false));
                     }
@@ -236,6 +269,9 @@ __global__ __launch_bounds__(1024) void w4_few_kernel(const W4FewParams p) {
                     for (int r = 0; r < RM; ++r) acc[r] = fmaf(s, P[r], acc[r]);
                 }
             }
+        const int j0 = (glu ? t >> 1 : t) * TR;  // the tile's first column
+        float* out = red_lane + (up * CT + j0) * RS;
+        const bool mine = (FULL || (n < 8 && q < 2)) && n < CT - j0;
 #pragma unroll
         for (int r = 0; r < RM; ++r) {
             float sum = acc[r];
@@ -244,9 +280,8 @@ __global__ __launch_bounds__(1024) void w4_few_kernel(const W4FewParams p) {
                 swap32(x, y);  // x: lanes 0-31 twice, y: lanes 32-63 twice
                 sum = __uint_as_float(x) + __int_as_float(dpp_mov<0x128>((int)y));
             }
-            const int m = FULL ? q + 4 * r : (q & 1) + 2 * r;
-            float* at = red + ((m * TT + t) * TR + n) * RS + wv;
-            if ((FULL || (n < 8 && q < 2)) && m < M) *at = add ? *at + sum : sum;
+            float* at = out + r * red_step;
+            if (mine && token0 + r * (FULL ? 4 : 2) < M) *at = add ? *at + sum : sum;
         }
     };
     for (int pass = 0; pass < p.passes; ++pass) {
@@ -256,25 +291,25 @@ __global__ __launch_bounds__(1024) void w4_few_kernel(const W4FewParams p) {
             const int k = k0 + l * 256 + half * 128 + q * 32;
             koff[l] = k < K ? k / 2 : 0;  // past K: any codes, x is zero there
         }
-        if (pass > 0) {
-            w4_lds_barrier();  // everyone is done with the last slice
-            stage_x(pass * KP);
-        }
+        if (pass > 0) stage_x(k0);  // this wave has read the last pass's
 #pragma unroll
         for (int t = 0; t < D; ++t) load_tile(t, t < TT ? t : TT - 1);
         __builtin_amdgcn_sched_barrier(0);
         w4_wait_vmcnt<D * PL * LH>();  // what was staged has arrived; the weights are on their way
-        w4_lds_barrier();
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        if (pass == 0) w4_lds_barrier();  // the scales and zero points of the others, too
 
         // A operands and X of this wave's lines
 #pragma unroll
         for (int l = 0; l < PL; ++l) {
-            const int ln = wv * PL + l;
-#pragma unroll
+            #pragma unroll
             for (int v = 0; v < LH; ++v) {
-                const int kh = ln * 256 + (FULL ? v : half) * 128;
+                const int sub = PL > 1 ? l : tok & 1;
+                const uint16_t* row = xw + (PL > 1 ? tok : tok >> 1) * kW4FewLoad + sub * 256;
+                const int first = (FULL ? v : half) * 16;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) a[l][v][j] = even_odd(*(const u32x4_t*)(xs + tok * XP + kh + lane_k(j)));
+                for (int j = 0; j < 4; ++j)
+                    a[l][v][j] = even_odd(*(const u32x4_t*)(row + place(first + lane_k(j) / 8, sub) * 8));
 #pragma unroll
                 for (int h = 0; h < UPH; ++h) {  // D is the same in every column; one writes it
                     f32x4v_t s = zero4;
@@ -300,14 +335,17 @@ __global__ __launch_bounds__(1024) void w4_few_kernel(const W4FewParams p) {
         for (; t + 2 * D <= TT; t += D) {
 #pragma unroll
             for (int i = 0; i < D; ++i) {
-                tile(i, t + i, pass > 0);
+                take(i);
                 load_tile(i, t + i + D);
+                tile(t + i, pass > 0);
             }
         }
 #pragma unroll
         for (int i = 0; i < 2 * D - 1; ++i) {
-            if (t + i < TT) tile(i % D, t + i, pass > 0);
+            if (t + i >= TT) break;
+            take(i % D);
             if (t + i + D < TT) load_tile(i % D, t + i + D);
+            tile(t + i, pass > 0);
         }
     }
     w4_lds_barrier();
@@ -317,7 +355,7 @@ __global__ __launch_bounds__(1024) void w4_few_kernel(const W4FewParams p) {
     for (int m = single ? 0 : wv; m < M; m += NW)
     for (int j = single ? tid : lane; j < CT; j += single ? NT : 64) {
         const int64_t c = c0 + j;
-        const float* src = red + ((m * TT + (glu ? (j / TR) * 2 : j / TR)) * TR + (j % TR)) * RS;
+        const float* src = red + (m * parts * CT + j) * RS;
         auto total = [&](const float* f) {
             f32x4v_t part[4];
 #pragma unroll
@@ -329,7 +367,7 @@ __global__ __launch_bounds__(1024) void w4_few_kernel(const W4FewParams p) {
         };
         float v = total(src);
         if (glu) {
-            const float v2 = total(src + TR * RS);
+            const float v2 = total(src + CT * RS);
             float av, dav;
             gate_act(v, p.act, av, dav);
             if (!p.dy) {

@@ -39,7 +39,7 @@ inline bool w4_few_plan(int64_t M, int64_t K, int64_t group, int64_t C, bool glu
                 const int64_t wrows = (rows + TR - 1) / TR * TR * (glu ? 2 : 1);
                 if (wrows >= 4096 || wrows * groups >= kW4LdsBytes) continue;
                 o.rows = (int)rows;
-                o.lds = w4_few_lds((int)M, U, o.pl, (int)wrows, (int)groups, o.nw).total;
+                o.lds = w4_few_lds((int)M, U, o.pl, (int)rows * (glu ? 2 : 1), (int)wrows, (int)groups, o.nw).total;
                 if (o.lds * per_cu > kW4LdsBytes && !(rows == 8 && o.lds <= kW4LdsBytes)) continue;
                 // about 20 to 32 KB a compute unit in flight (17408 x 5120, 10 waves: one tile ahead 11.2 us,
                 // two 11.8; 28672 x 4096 gated, 8 waves: 14.9 and 13.1)
