@@ -15,8 +15,13 @@
 // 16 bytes, of which lane half h takes dwords 2h and 2h + 1, one for each of
 // two matrix instructions, and x is read in the same order.  Codes are
 // dequantised in registers on the way, rounded once to the 16-bit type.  The
-// waves' sums are added in wave order through LDS at the end, 16 or 8
-// tokens at a time.
+// waves' sums are added in wave order through the first stage's LDS at the
+// end, 16 or 8 tokens at a time.
+//
+// Measured (weights cold): 48 tokens, 4096 x 4096 14.3 us, 8192 x 8192 27.2,
+// 2 x 2051 x 7168 gated 21.4; 64 tokens, 17408 x 5120 36.9 us.  With few rows
+// half the compute units are idle, and a step takes what its token rows take
+// to arrive: 0.36 us with 32 of them, 0.5 with 48, 0.6 with 64.
 #pragma once
 #include "w4_device.hpp"
 #include "w4_launch.hpp"
@@ -35,25 +40,27 @@ struct W4MidParams {
 
 constexpr int kW4MidStep = 256;
 
-template <int BM, int BN>
-constexpr int w4_mid_stage() { return (BM * 2 + BN / 2) * kW4MidStep; }
+constexpr int w4_mid_stage(int XR, int NTL) { return (XR * 2 + NTL * 16) * kW4MidStep; }
+// tokens whose sums are added at a time: the waves' sums take the first stage's LDS
+constexpr int w4_mid_parts(int NTL) { return NTL > 1 ? 8 : 16; }
 
 // scales and zero points of the workgroup's rows, as in memory from the 16-byte line each block starts in
 inline __host__ __device__ uint32_t w4_mid_scales(int rows, int groups) {
     return ((uint32_t)(rows * groups * 2) + 15u) / 16u * 16u + ((uint32_t)(rows * groups) + 15u) / 16u * 16u + 128u;
 }
 
-template <int T, int MT, int NTL, int STAGES>  // 2 <= STAGES <= 4
+template <int T, int XR, int NTL, int STAGES>  // XR: token rows staged, 32, 48 or 64; 2 <= STAGES <= 4
 __global__ __launch_bounds__(512) void w4_mid_kernel(const W4MidParams p) {
-    constexpr int BM = 32 * MT, BN = 32 * NTL, NW = 8, NT = 512, STEP = kW4MidStep;
-    constexpr int XI = BM / 2 / NW;                   // x loads of a wave and step: 2 rows of 512 bytes each
+    constexpr int MT = (XR + 31) / 32, BM = 32 * MT, BN = 32 * NTL, NW = 8, NT = 512, STEP = kW4MidStep;
+    constexpr int XI = XR / 2 / NW;                   // x loads of a wave and step: 2 rows of 512 bytes each
     constexpr int WL = BN / 8;                        // code loads of a step: 8 rows of 128 bytes each
     constexpr int WI = (WL + NW - 1) / NW;            // of a wave; the last only of waves below WL % NW
-    constexpr int ST = w4_mid_stage<BM, BN>();
+    constexpr int ST = w4_mid_stage(XR, NTL);
     extern __shared__ __align__(16) uint8_t w4m_lds[];  // scales
     __shared__ __align__(16) uint8_t st0[ST], st1[ST], st2[STAGES > 2 ? ST : 16], st3[STAGES > 3 ? ST : 16];
-    constexpr int RT = NTL > 2 ? 8 : 16;                // tokens whose sums are added at a time
-    __shared__ float red[NW * RT * BN];                 // [wave][token % RT][row]
+    constexpr int RT = w4_mid_parts(NTL);
+    static_assert(NW * RT * BN * 4 <= ST, "the sums fit a stage");
+    float* red = (float*)st0;                           // after the last step: [wave][token % RT][row]
 
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, G = p.groups;
     const int64_t m0 = (int64_t)blockIdx.y * BM;
@@ -129,7 +136,7 @@ __global__ __launch_bounds__(512) void w4_mid_kernel(const W4MidParams p) {
 #pragma unroll
         for (int i = 0; i < WI; ++i) {  // past K: zero codes, and x is zero there
             const void* src = k0 + wk[i] < K ? (const void*)(wsrc[i] + k0 / 2) : (const void*)&kW4Zero16;
-            uint8_t* dst = base + BM * STEP * 2 + (i * NW + wv) * 1024;
+            uint8_t* dst = base + XR * STEP * 2 + (i * NW + wv) * 1024;
             if (i + 1 < WI || full) __builtin_amdgcn_global_load_lds(src, (lds_void_t*)dst, 16, 0, 0);
         }
     };
@@ -151,7 +158,25 @@ __global__ __launch_bounds__(512) void w4_mid_kernel(const W4MidParams p) {
 #pragma unroll
         for (int t = 0; t < NTL; ++t) acc[m][t] = f32x16v_t{};
 
-    // step s on stage `xt`; the stage that step s - 1 used is filled again
+    struct Operands { u32x4_t a[MT][2]; uint2 q[NTL]; uint32_t s[NTL], z[NTL]; };
+    Operands now;
+    auto multiply = [&]() {
+#pragma unroll
+        for (int t = 0; t < NTL; ++t) {
+            W4Scale<T> sc;
+            sc.set(now.s[t], has_z ? now.z[t] : 8u);
+            const u32x4_t b0 = sc.weights8(now.q[t].x), b1 = sc.weights8(now.q[t].y);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                acc[m][t] = mfma32<T>(now.a[m][0], b0, acc[m][t]);
+                acc[m][t] = mfma32<T>(now.a[m][1], b1, acc[m][t]);
+            }
+        }
+    };
+
+    // step s on stage `xt`: its operands are read while those of step s - 1 are multiplied, where registers hold both
+    // (48 tokens, 8192 x 8192, two row tiles: 29.6 and 27.3 us), and the stage that step s - 1 used is filled again
+    constexpr bool kAhead = NTL <= 2;
     auto step = [&](int s, const uint8_t* xt, uint8_t* refill) {
         // this wave's loads of step s have arrived once at most those of the next STAGES - 2 steps are left
         if (s + STAGES - 2 < steps) {
@@ -161,37 +186,29 @@ __global__ __launch_bounds__(512) void w4_mid_kernel(const W4MidParams p) {
             w4_wait_vmcnt<0>();
         }
         w4_lds_barrier();  // step s is complete for everyone, and everyone is done with step s - 1
-        const uint8_t* wt = xt + BM * STEP * 2;
+        const uint8_t* wt = xt + XR * STEP * 2;
         uint32_t g = (uint32_t)(s * (STEP / 32) + wv);
         if (p.ratio_magic) g = __umulhi(g, p.ratio_magic);
         if ((int)g >= G) g = G - 1;  // past K
-        u32x4_t a[MT][2];
+        Operands next;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-                const int r = m * 32 + row;
-                a[m][ks] = *(const u32x4_t*)(xt + r * (STEP * 2) + (((wv * 4 + 2 * half + ks) ^ (r & 31)) * 16));
+                const int r = m * 32 + row < XR ? m * 32 + row : XR - 1;  // past the staged rows: not stored
+                next.a[m][ks] = *(const u32x4_t*)(xt + r * (STEP * 2) + (((wv * 4 + 2 * half + ks) ^ (r & 31)) * 16));
             }
-        uint2 q[NTL];
-        W4Scale<T> sc[NTL];
 #pragma unroll
         for (int t = 0; t < NTL; ++t) {
             const int lr = lrow[t];
-            q[t] = *(const uint2*)(wt + lr * (STEP / 2) + ((wv ^ (lr & 7)) * 16) + half * 8);
-            const uint32_t sv = *(const uint16_t*)(w4m_lds + sbase[t] + g * 2), zv = w4m_lds[zbase[t] + g];
-            sc[t].set(sv, has_z ? zv : 8u);
+            next.q[t] = *(const uint2*)(wt + lr * (STEP / 2) + ((wv ^ (lr & 7)) * 16) + half * 8);
+            next.s[t] = *(const uint16_t*)(w4m_lds + sbase[t] + g * 2);
+            next.z[t] = w4m_lds[zbase[t] + g];
         }
         if (s + STAGES - 1 < steps) issue(s + STAGES - 1, refill);
-#pragma unroll
-        for (int t = 0; t < NTL; ++t) {
-            const u32x4_t b0 = sc[t].weights8(q[t].x), b1 = sc[t].weights8(q[t].y);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                acc[m][t] = mfma32<T>(a[m][0], b0, acc[m][t]);
-                acc[m][t] = mfma32<T>(a[m][1], b1, acc[m][t]);
-            }
-        }
+        if (kAhead && s > 0) multiply();
+        now = next;
+        if (!kAhead) multiply();
     };
     uint8_t* const ring[4] = {st0, st1, st2, st3};
 #pragma unroll
@@ -204,6 +221,8 @@ __global__ __launch_bounds__(512) void w4_mid_kernel(const W4MidParams p) {
     }
 
     // ---- sums of the waves, in order, RT tokens at a time: register e of a tile is token 8(e/4) + 4*half + e%4
+    if (kAhead) multiply();
+    w4_lds_barrier();  // everyone is done with the stages; no load into them is left
 #pragma unroll
     for (int part = 0; part < BM / RT; ++part) {
         if (part * RT >= M) break;  // workgroup-uniform

@@ -5,7 +5,7 @@
 
 namespace qlin {
 
-struct W4MidPlan { int ntl; uint32_t scales; float us; };  // row tiles, LDS of the scales, estimated time
+struct W4MidPlan { int ntl, stages; uint32_t scales; float us; };  // row tiles, LDS of the scales, estimated time
 
 // false if the scales of 32 rows do not fit LDS next to two stages
 bool w4_mid_plan(int64_t M, int64_t K, int64_t group, int64_t C, bool glu, W4MidPlan& o);
