@@ -150,8 +150,9 @@ BwdPlan bwd_plan(int64_t M, int64_t N, int64_t K) {
     if (M <= 64) {
         o.cw = M <= 32 ? 16 : 8;
         const int64_t cols = (K + 16 * o.cw - 1) / (16 * o.cw), blocks = (N + 31) / 32;
-        // about 1024 workgroups of 4 waves, at least one block a wave
-        int64_t shares = 512 / cols;
+        // one workgroup of 4 waves a compute unit, at least one block a wave (33 tokens, 4096 x 7168: 20 us, two 22,
+        // half of one 28; one token, 17408 x 5120: 25, 24.4 and 39)
+        int64_t shares = 256 / cols;
         if (shares > (blocks + 3) / 4) shares = (blocks + 3) / 4;
         o.per = shares > 1 ? (blocks + shares - 1) / shares : blocks;
         o.shares = (blocks + o.per - 1) / o.per;
