@@ -378,6 +378,8 @@ def qlin_moe_ffn_mxfp4(x, wr, w13, s13, w2, s2, topk, alpha=1.0, limit=10.0, y=N
 # ----------------------------------------------------------------------------- 4-bit weights with group scales
 # One token through a small layer is a few microseconds on the GPU, so these calls look at each tensor
 # only as often as the checks need; _w4_weight says what was wrong once a check has failed.
+# `stream`: a torch.cuda.Stream (results and workspaces that are not supplied come from its memory) or a raw
+# handle (every one of them is supplied, unless the handle is the current stream's).
 
 _DT16 = {torch.bfloat16: QLIN_DT_BF16, torch.float16: QLIN_DT_FP16}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -414,10 +416,33 @@ def _w4_weight(a, name, w, ws, wz):
     raise ValueError(f"w, ws and wz must be on {name}'s device, {a.device}")
 
 
-def _out16(t, name, like, rows, cols):
+def _own(name, shape, dtype, like, stream):
+    """Memory of the call's own on the stream that its kernels run on.
+
+    A block belongs to the stream it was allocated on: taken from the current one it may still be written by work
+    queued there, and once dropped it is handed out there again, while the kernels on `stream` are using it.  The
+    caller meets the result on the current stream, so that one is recorded, too.  Behind a raw handle there is no
+    pool to take memory from; one that is the current stream's needs none."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    here = torch.cuda.current_stream(like.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        if stream != here.cuda_stream:
+            raise ValueError(f"a raw stream that is not the current one needs {name} along with it, {tuple(shape)}")
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if stream.device != like.device:
+        raise ValueError(f"stream is on {stream.device}, the operands on {like.device}")
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    if stream != here:
+        t.record_stream(here)
+    return t
+
+
+def _out16(t, name, like, rows, cols, stream=None):
     """An operand or output of `like`'s type and device: allocated if None, or checked."""
     if t is None:
-        return torch.empty((rows, cols), dtype=like.dtype, device=like.device)
+        return _own(name, (rows, cols), like.dtype, like, stream)
     if (t.dtype is like.dtype and t.dim() == 2 and t.shape[0] == rows and t.shape[1] == cols
             and (t.stride(1) == 1 or cols == 1) and t.get_device() == like.get_device()):
         return t
@@ -463,7 +488,7 @@ def qlin_gemv_w4(x, w, ws, wz=None, bias=None, y=None, stream=None):
         _need(bias, "bias", (x.dtype,), 1)
         if bias.shape[0] != N or bias.get_device() != dev:
             raise ValueError(f"bias must be [{N}] on {x.device}")
-    y = _out16(y, "y", x, M, N)
+    y = _out16(y, "y", x, M, N, stream)
     _launch(load().qlin_gemv_w4, "qlin_gemv_w4", dev, stream, x.data_ptr(), _pitch(x, M, K), M, K, dt, w.data_ptr(),
             _wpitch(w), N, ws.data_ptr(), _ptr(wz), group, _ptr(bias), y.data_ptr(), _pitch(y, M, N))
     return y
@@ -479,10 +504,7 @@ def _w4_workspace(workspace, M, N, K, like, stream):
     if workspace is None:
         if not need:
             return None, 0
-        if stream is not None and not isinstance(stream, torch.cuda.Stream):
-            raise ValueError(f"a raw stream needs a workspace of {need} bytes along with it")
-        with torch.cuda.stream(stream):  # None: the current one
-            workspace = torch.empty((need,), dtype=torch.uint8, device=like.device)
+        workspace = _own("a workspace", (need,), torch.uint8, like, stream)
     elif workspace.get_device() != like.get_device() or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on {like.device}")
     return workspace, workspace.numel() * workspace.element_size()
@@ -495,7 +517,7 @@ def qlin_gemv_w4_bwd(dy, w, ws, wz=None, dx=None, workspace=None, stream=None):
     M, Ny = dy.shape
     if Ny != N:
         raise ValueError(f"w has N={N}, dy has N={Ny}")
-    dx = _out16(dx, "dx", dy, M, K)
+    dx = _out16(dx, "dx", dy, M, K, stream)
     buf, size = _w4_workspace(workspace, M, N, K, dy, stream)
     _launch(load().qlin_gemv_w4_bwd, "qlin_gemv_w4_bwd", dev, stream, dy.data_ptr(), _pitch(dy, M, N), M, N, dt,
             w.data_ptr(), _wpitch(w), K, ws.data_ptr(), _ptr(wz), group, dx.data_ptr(), _pitch(dx, M, K), _ptr(buf), size)
@@ -511,7 +533,7 @@ def qlin_glu_w4(x, w13, s13, z13=None, act=QLIN_ACT_SILU, y=None, gu=None, strea
     I = N // 2
     if Kx != K or N != 2 * I:
         raise ValueError(f"w13 is [{N}, {K}], x has K={Kx}: rows must be 2I, K equal")
-    y = _out16(y, "y", x, M, I)
+    y = _out16(y, "y", x, M, I, stream)
     if gu is not None:
         _out16(gu, "gu", x, M, N)
     _launch(load().qlin_glu_w4, "qlin_glu_w4", dev, stream, x.data_ptr(), _pitch(x, M, K), M, K, dt, w13.data_ptr(),
@@ -536,12 +558,12 @@ def qlin_glu_w4_bwd(dy, w13, s13, z13=None, act=QLIN_ACT_SILU, x=None, gu=None, 
     if gu is not None:
         _out16(gu, "gu", dy, M, N)
     if dgu is None:  # row pitch a multiple of 8, as the second product reads it
-        dgu = torch.empty((M, (N + 7) // 8 * 8), dtype=dy.dtype, device=dy.device)[:, :N]
+        dgu = _own("dgu", (M, (N + 7) // 8 * 8), dy.dtype, dy, stream)[:, :N]
     else:
         _out16(dgu, "dgu", dy, M, N)
     buf, size = None, 0
     if need_dx:
-        dx = _out16(dx, "dx", dy, M, K)
+        dx = _out16(dx, "dx", dy, M, K, stream)
         buf, size = _w4_workspace(workspace, M, N, K, dy, stream)
     else:
         dx = None
