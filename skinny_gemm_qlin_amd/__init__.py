@@ -5,7 +5,8 @@ functions carry the C names and only marshal arguments: they check dtype,
 device and that the innermost dimension is contiguous, pass data pointers,
 row pitches and torch's current HIP stream, and raise QlinError on a non-zero
 status.  Outputs that are not supplied are allocated with torch (device
-memory plumbing only).  Every arithmetic step runs in the HIP kernels.
+memory plumbing only), in memory of the stream that the call runs on.  Every
+arithmetic step runs in the HIP kernels.
 
 Storage conventions: bf16 tensors are torch.bfloat16; int8 codes are
 torch.int8; E4M3 codes, UE8M0 scale bytes and packed E2M1 nibbles are
@@ -47,6 +48,35 @@ def _need(t: torch.Tensor, name: str, dtypes, dims: int):
     return t
 
 
+def _own(name, shape, dtype, like, stream):
+    """Memory of the call's own on the stream that its kernels run on: a torch.cuda.Stream or a raw handle, None
+    for the current one.
+
+    A block belongs to the stream it was allocated on: taken from the current one it may still be written by work
+    queued there, and once dropped it is handed out there again, while the kernels on `stream` are using it.  The
+    caller meets the result on the current stream, so that one is recorded, too.  `name`, if given, is what the
+    caller has to supply along with a raw handle that is not the current stream's; without a name torch keeps
+    memory for the handle as it does for an external stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    here = torch.cuda.current_stream(like.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = getattr(stream, "cuda_stream", stream)
+        if raw == here.cuda_stream:
+            return torch.empty(shape, dtype=dtype, device=like.device)
+        if name:
+            raise ValueError(f"a raw stream that is not the current one needs {name} along with it, {tuple(shape)}")
+        stream = (torch.cuda.ExternalStream(raw, device=like.device) if raw
+                  else torch.cuda.default_stream(like.device))
+    elif stream.device != like.device:
+        raise ValueError(f"stream is on {stream.device}, the operands on {like.device}")
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    if stream != here:
+        t.record_stream(here)
+    return t
+
+
 _U8 = (torch.uint8, torch.float8_e4m3fn)
 
 
@@ -55,9 +85,9 @@ def qlin_act_quant_i8(x, xq=None, xs=None, stream=None):
     _need(x, "x", (torch.bfloat16,), 2)
     M, K = x.shape
     if xq is None:
-        xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        xq = _own(None, (M, K), torch.int8, x, stream)
     if xs is None:
-        xs = torch.empty((M,), dtype=torch.float32, device=x.device)
+        xs = _own(None, (M,), torch.float32, x, stream)
     _need(xq, "xq", (torch.int8,), 2)
     _need(xs, "xs", (torch.float32,), 1)
     check(load().qlin_act_quant_i8(x.data_ptr(), x.stride(0), M, K, xq.data_ptr(), xq.stride(0),
@@ -80,7 +110,7 @@ def qlin_gemv_i8(xq, xs, w, ws, bias=None, y=None, out_kind=0, stream=None):
     if bias is not None:
         _need(bias, "bias", (torch.bfloat16,), 1)
     if y is None:
-        y = torch.empty((M, N), dtype=torch.int32 if out_kind == 1 else torch.bfloat16, device=xq.device)
+        y = _own(None, (M, N), torch.int32 if out_kind == 1 else torch.bfloat16, xq, stream)
     _need(y, "y", (torch.int32,) if out_kind == 1 else (torch.bfloat16,), 2)
     check(load().qlin_gemv_i8(xq.data_ptr(), xq.stride(0), xs.data_ptr(), int(xs.numel() > 1), M, K,
                               w.data_ptr(), w.stride(0), N, ws.data_ptr(), int(ws.numel() > 1),
@@ -104,11 +134,11 @@ def qlin_linear_i8(x, w, ws, bias=None, xq=None, xs=None, y=None, stream=None):
     if bias is not None:
         _need(bias, "bias", (torch.bfloat16,), 1)
     if xq is None:
-        xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        xq = _own(None, (M, K), torch.int8, x, stream)
     if xs is None:
-        xs = torch.empty((M,), dtype=torch.float32, device=x.device)
+        xs = _own(None, (M,), torch.float32, x, stream)
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        y = _own(None, (M, N), torch.bfloat16, x, stream)
     _need(xq, "xq", (torch.int8,), 2)
     _need(xs, "xs", (torch.float32,), 1)
     _need(y, "y", (torch.bfloat16,), 2)
@@ -129,7 +159,7 @@ def qlin_gemv_fp8(x, w, ws, y=None, stream=None):
     if w.shape[1] != K:
         raise ValueError(f"w has K={w.shape[1]}, x has K={K}")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        y = _own(None, (M, N), torch.bfloat16, x, stream)
     _need(y, "y", (torch.bfloat16,), 2)
     check(load().qlin_gemv_fp8(x.data_ptr(), x.stride(0), M, K, w.data_ptr(), w.stride(0), N,
                                ws.data_ptr(), int(ws.numel() > 1), y.data_ptr(), y.stride(0),
@@ -154,9 +184,9 @@ def qlin_act_quant_fp8(x, fmt=QLIN_FMT_E4M3, per_token=True, xq=None, xs=None, s
     _need(x, "x", (torch.bfloat16,), 2)
     M, K = x.shape
     if xq is None:
-        xq = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+        xq = _own(None, (M, K), torch.uint8, x, stream)
     if xs is None:
-        xs = torch.empty((M if per_token else 1,), dtype=torch.float32, device=x.device)
+        xs = _own(None, (M if per_token else 1,), torch.float32, x, stream)
     _codes(xq, "xq", fmt)
     _need(xs, "xs", (torch.float32,), 1)
     if xs.numel() < (M if per_token else 1):
@@ -181,7 +211,7 @@ def qlin_gemv_fp8_w8a8(xq, xs, w, ws, x_fmt=QLIN_FMT_E4M3, w_fmt=QLIN_FMT_E4M3, 
     if xs.numel() not in (1, M) or ws.numel() not in (1, N):
         raise ValueError(f"xs must hold 1 or M={M} scales, ws 1 or N={N}")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
+        y = _own(None, (M, N), torch.bfloat16, xq, stream)
     _need(y, "y", (torch.bfloat16,), 2)
     check(load().qlin_gemv_fp8_w8a8(xq.data_ptr(), xq.stride(0), xs.data_ptr(), int(xs.numel() > 1),
                                     int(x_fmt), M, K, w.data_ptr(), w.stride(0), N, ws.data_ptr(),
@@ -198,7 +228,7 @@ def qlin_gemv_fp8_blk(x, w, ws, xq=None, xs=None, y=None, stream=None, export=Tr
     if not export:
         _need(x, "x", (torch.bfloat16,), 2)
         if y is None:
-            y = torch.empty((x.shape[0], w.shape[0]), dtype=torch.bfloat16, device=x.device)
+            y = _own(None, (x.shape[0], w.shape[0]), torch.bfloat16, x, stream)
         check(load().qlin_gemv_fp8_blk(x.data_ptr(), x.stride(0), x.shape[0], x.shape[1], w.data_ptr(),
                                        w.stride(0), w.shape[0], ws.data_ptr(), None, None, y.data_ptr(),
                                        y.stride(0), _stream(x, stream)), "qlin_gemv_fp8_blk")
@@ -213,11 +243,11 @@ def qlin_gemv_fp8_blk(x, w, ws, xq=None, xs=None, y=None, stream=None, export=Tr
     if tuple(ws.shape) != ((N + 127) // 128, K // 128) or not ws.is_contiguous():
         raise ValueError(f"ws must be contiguous [{(N + 127) // 128}, {K // 128}], got {tuple(ws.shape)}")
     if xq is None:
-        xq = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+        xq = _own(None, (M, K), torch.uint8, x, stream)
     if xs is None:
-        xs = torch.empty((M, K // 128), dtype=torch.uint8, device=x.device)
+        xs = _own(None, (M, K // 128), torch.uint8, x, stream)
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        y = _own(None, (M, N), torch.bfloat16, x, stream)
     if not xq.is_contiguous() or not xs.is_contiguous():
         raise ValueError("xq / xs must be contiguous")
     _need(y, "y", (torch.bfloat16,), 2)
@@ -240,11 +270,11 @@ def qlin_gemv_fp8_blk_ex(x, w, ws, block_n, block_k, xq=None, xs=None, y=None, s
     if tuple(ws.shape) != ((N + block_n - 1) // block_n, K // block_k) or not ws.is_contiguous():
         raise ValueError(f"ws must be contiguous [{(N + block_n - 1) // block_n}, {K // block_k}], got {tuple(ws.shape)}")
     if xq is None:
-        xq = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+        xq = _own(None, (M, K), torch.uint8, x, stream)
     if xs is None:
-        xs = torch.empty((M, K // block_k), dtype=torch.uint8, device=x.device)
+        xs = _own(None, (M, K // block_k), torch.uint8, x, stream)
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        y = _own(None, (M, N), torch.bfloat16, x, stream)
     if not xq.is_contiguous() or not xs.is_contiguous():
         raise ValueError("xq / xs must be contiguous")
     _need(y, "y", (torch.bfloat16,), 2)
@@ -278,9 +308,9 @@ def qlin_moe_mxfp4(x, w, s, topk_ids, topk_w, y=None, workspace=None, stream=Non
         raise ValueError("topk_ids / topk_w must be [M, topk]")
     need = qlin_moe_mxfp4_workspace_bytes(M, N, topk, E)
     if workspace is None:
-        workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=x.device)
+        workspace = _own(None, (max(need, 1),), torch.uint8, x, stream)
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        y = _own(None, (M, N), torch.bfloat16, x, stream)
     _need(y, "y", (torch.bfloat16,), 2)
     check(load().qlin_moe_mxfp4(x.data_ptr(), x.stride(0), M, K, w.data_ptr(), s.data_ptr(), E, N,
                                 topk_ids.data_ptr(), topk_w.data_ptr(), topk, y.data_ptr(), y.stride(0),
@@ -349,14 +379,14 @@ def qlin_moe_ffn_mxfp4(x, wr, w13, s13, w2, s2, topk, alpha=1.0, limit=10.0, y=N
         raise ValueError("router / expert tensor shapes do not match x")
     need = qlin_moe_ffn_mxfp4_workspace_bytes(M, H, I, topk, E)
     if workspace is None:
-        workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=x.device)
+        workspace = _own(None, (max(need, 1),), torch.uint8, x, stream)
     if y is None:
-        y = torch.empty((M, H), dtype=torch.bfloat16, device=x.device)
+        y = _own(None, (M, H), torch.bfloat16, x, stream)
     _need(y, "y", (torch.bfloat16,), 2)
     if ids is None:
-        ids = torch.empty((M, topk), dtype=torch.int32, device=x.device)
+        ids = _own(None, (M, topk), torch.int32, x, stream)
     if gw is None:
-        gw = torch.empty((M, topk), dtype=torch.float32, device=x.device)
+        gw = _own(None, (M, topk), torch.float32, x, stream)
     _need(ids, "ids", (torch.int32,), 2)
     _need(gw, "gw", (torch.float32,), 2)
     if tuple(ids.shape) != (M, topk) or tuple(gw.shape) != (M, topk) or not (ids.is_contiguous() and gw.is_contiguous()):
@@ -414,29 +444,6 @@ def _w4_weight(a, name, w, ws, wz):
         if wz.shape != ws.shape or not wz.is_contiguous():
             raise ValueError(f"wz must be contiguous {tuple(ws.shape)}, got {tuple(wz.shape)}")
     raise ValueError(f"w, ws and wz must be on {name}'s device, {a.device}")
-
-
-def _own(name, shape, dtype, like, stream):
-    """Memory of the call's own on the stream that its kernels run on.
-
-    A block belongs to the stream it was allocated on: taken from the current one it may still be written by work
-    queued there, and once dropped it is handed out there again, while the kernels on `stream` are using it.  The
-    caller meets the result on the current stream, so that one is recorded, too.  Behind a raw handle there is no
-    pool to take memory from; one that is the current stream's needs none."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    here = torch.cuda.current_stream(like.device)
-    if not isinstance(stream, torch.cuda.Stream):
-        if stream != here.cuda_stream:
-            raise ValueError(f"a raw stream that is not the current one needs {name} along with it, {tuple(shape)}")
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    if stream.device != like.device:
-        raise ValueError(f"stream is on {stream.device}, the operands on {like.device}")
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=like.device)
-    if stream != here:
-        t.record_stream(here)
-    return t
 
 
 def _out16(t, name, like, rows, cols, stream=None):
