@@ -180,22 +180,24 @@ __device__ __forceinline__ void w4_wait_vmcnt() {  // s_waitcnt vmcnt(N_), other
 // q = 1 - p the derivative is p + g p q dv/dg, v the logistic's argument.
 // v_exp_f32 and v_rcp_f32 (1 ulp) are well inside the 16-bit output rounding.
 // |g| is cut at 30 for gelu's argument (p and q are 0 or 1 there to every
-// digit, and g^3 cannot overflow); silu's e^-g may be infinite, p is then 0.
+// digit, and g^3 cannot overflow), by comparisons that leave a NaN one.  Where
+// p or q is 0 its product with g is 0 too: g may be infinite there, as a gate
+// beyond fp16's range is once it has been kept.
 __device__ __forceinline__ void gate_act(float g, int act, float& a, float& da) {
     float v, dv;
     if (act == kActSilu) {
         v = g;
         dv = 1.0f;
     } else {
-        const float c = fminf(fmaxf(g, -30.0f), 30.0f), cc = c * c;
+        const float c = g > 30.0f ? 30.0f : (g < -30.0f ? -30.0f : g), cc = c * c;
         v = 1.5957691216057308f * (c + 0.044715f * c * cc);
         dv = 1.5957691216057308f * (1.0f + 0.134145f * cc);
     }
     const float e = __expf(-fabsf(v));                    // in (0, 1]
     const float r = __builtin_amdgcn_rcpf(1.0f + e);      // the larger of p and q
     const float p = v >= 0.0f ? r : e * r, q = v >= 0.0f ? e * r : r;
-    a = g * p;
-    da = fmaf(g * p * q, dv, p);
+    a = p == 0.0f ? -0.0f : g * p;
+    da = fmaf(q == 0.0f ? 0.0f : a * q, dv, p);
 }
 
 }  // namespace qlin
