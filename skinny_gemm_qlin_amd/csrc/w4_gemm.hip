@@ -1,4 +1,6 @@
 // w4_gemm.hip -- launchers of the 4-bit weight GEMM (w4_gemm.hpp).
+#include <algorithm>
+
 #include "w4_few_launch.hpp"
 #include "w4_mid_launch.hpp"
 #include "w4_bwd.hpp"
@@ -225,7 +227,7 @@ hipError_t launch_gate_bwd(const W4GateBwdArgs& a, hipStream_t st) {
     const bool vec = a.I % 8 == 0 && (((uintptr_t)a.dy | (uintptr_t)a.gu | (uintptr_t)a.dgu) & 15) == 0 &&
                      (a.lddy | a.ldgu | a.lddgu) % 8 == 0;
     const int64_t n = a.M * (vec ? a.I / 8 : a.I);
-    const dim3 grid((unsigned)((n + 255) / 256));
+    const dim3 grid((unsigned)std::min((n + 255) / 256, kW4GateBlocks));
     if (a.dtype == kFp16) {
         if (vec) hipLaunchKernelGGL((w4_gate_bwd_kernel<kFp16, 8>), grid, dim3(256), 0, st, a);
         else hipLaunchKernelGGL((w4_gate_bwd_kernel<kFp16, 1>), grid, dim3(256), 0, st, a);

@@ -414,37 +414,41 @@ __global__ __launch_bounds__(256) void w4_reduce_kernel(const float* part, int64
     for (int e = 0; e < V; ++e) y[m * ldy + c + e] = f32_to_h<T>(sum[e]);
 }
 
-// dgu = [dy u act'(g), dy act(g)], V columns a thread
+// dgu = [dy u act'(g), dy act(g)], V columns a thread; a grid of at most kW4GateBlocks workgroups, which then take
+// more than one turn (a launch holds fewer than 2^32 threads, M * I may be more)
+constexpr int64_t kW4GateBlocks = 1 << 22;
+
 template <int T, int V>
 __global__ __launch_bounds__(256) void w4_gate_bwd_kernel(const W4GateBwdArgs a) {
-    const int64_t per = a.I / V, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= a.M * per) return;
-    const int64_t m = i / per, c = (i - m * per) * V;
+    const int64_t per = a.I / V;
     typedef uint16_t vec_t __attribute__((ext_vector_type(V)));
-    vec_t d, g, u, og, ou;
-    if constexpr (V == 1) {
-        d[0] = a.dy[m * a.lddy + c];
-        g[0] = a.gu[m * a.ldgu + c];
-        u[0] = a.gu[m * a.ldgu + a.I + c];
-    } else {
-        d = *(const vec_t*)(a.dy + m * a.lddy + c);
-        g = *(const vec_t*)(a.gu + m * a.ldgu + c);
-        u = *(const vec_t*)(a.gu + m * a.ldgu + a.I + c);
-    }
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.M * per; i += (int64_t)gridDim.x * 256) {
+        const int64_t m = i / per, c = (i - m * per) * V;
+        vec_t d, g, u, og, ou;
+        if constexpr (V == 1) {
+            d[0] = a.dy[m * a.lddy + c];
+            g[0] = a.gu[m * a.ldgu + c];
+            u[0] = a.gu[m * a.ldgu + a.I + c];
+        } else {
+            d = *(const vec_t*)(a.dy + m * a.lddy + c);
+            g = *(const vec_t*)(a.gu + m * a.ldgu + c);
+            u = *(const vec_t*)(a.gu + m * a.ldgu + a.I + c);
+        }
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        float av, dav;
-        const float dv = h_to_f32<T>(d[e]);
-        gate_act(h_to_f32<T>(g[e]), a.act, av, dav);
-        og[e] = f32_to_h<T>(dv * h_to_f32<T>(u[e]) * dav);
-        ou[e] = f32_to_h<T>(dv * av);
-    }
-    if constexpr (V == 1) {
-        a.dgu[m * a.lddgu + c] = og[0];
-        a.dgu[m * a.lddgu + a.I + c] = ou[0];
-    } else {
-        *(vec_t*)(a.dgu + m * a.lddgu + c) = og;
-        *(vec_t*)(a.dgu + m * a.lddgu + a.I + c) = ou;
+        for (int e = 0; e < V; ++e) {
+            float av, dav;
+            const float dv = h_to_f32<T>(d[e]);
+            gate_act(h_to_f32<T>(g[e]), a.act, av, dav);
+            og[e] = f32_to_h<T>(dv * h_to_f32<T>(u[e]) * dav);
+            ou[e] = f32_to_h<T>(dv * av);
+        }
+        if constexpr (V == 1) {
+            a.dgu[m * a.lddgu + c] = og[0];
+            a.dgu[m * a.lddgu + a.I + c] = ou[0];
+        } else {
+            *(vec_t*)(a.dgu + m * a.lddgu + c) = og;
+            *(vec_t*)(a.dgu + m * a.lddgu + a.I + c) = ou;
+        }
     }
 }
 

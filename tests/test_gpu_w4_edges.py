@@ -56,3 +56,27 @@ def test_gates_below_the_lowest_fp16(ql, M, act):
     for kept in ({"gu": gu}, {"x": x}):
         dx, dgu = ql.qlin_glu_w4_bwd(dy, *layer, act=act, **kept)
         assert bool((dgu == 0).all()) and bool((dx == 0).all())
+
+
+def test_more_gates_than_a_launch_has_threads(ql):
+    """M * I past 2^32 with an odd I (one column a thread), in place: rows at both ends and across 2^32."""
+    M, I, dt = 16384, (1 << 18) + 1, torch.bfloat16
+    w, ws, wz = gen_w4(2 * I, 32, 32, "bf16", False, seed=1)
+    layer = dev_w(w, ws, wz)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(1)
+    buf = torch.empty((M, 2 * I + 6), dtype=dt, device="cuda").normal_(generator=gen)
+    gu = buf[:, :2 * I]
+    dy = torch.empty((M, I), dtype=dt, device="cuda").normal_(generator=gen)
+    rows = [0, 1, 4095, 8191, 8192, M - 3, M - 2, M - 1]
+    before, pads = gu[rows].double(), buf[:, 2 * I:].clone()
+    _, dgu = ql.qlin_glu_w4_bwd(dy, *layer, gu=gu, dgu=gu, need_dx=False)
+    assert dgu.data_ptr() == gu.data_ptr()
+    g, u, d = before[:, :I], before[:, I:], dy[rows].double()
+    s = torch.sigmoid(g)
+    want = torch.cat((d * u * (s + g * s * (1 - s)), d * g * s), dim=1)
+    # one rounding (2^-8) of a product of fp32 terms: 64 ulps of 2^-24 times |g| <= 6 stay below 2^-14 of |d u| or |d g|
+    slack = torch.cat((d * u, d * g), dim=1).abs() * 2.0 ** -14
+    got = dgu[rows].double()
+    assert bool(((got - want).abs() <= want.abs() * 2.0 ** -8 + slack).all())
+    assert torch.equal(buf[:, 2 * I:], pads)
