@@ -27,7 +27,7 @@ SOURCES = ["gemv.hip", "ks_i8.hip", "ks_f8.hip", "ks_w8a8_e4m3.hip", "ks_w8a8_e5
            "w4_few_bf16.hip", "w4_few_fp16.hip", "w4_mid.hip", "gemm.hip", "moe.hip", "moe_prefill.hip", "routing.hip"]
 HEADERS = ["qlin_device.hpp", "qlin_launch.hpp", "gemv_kernels.hpp", "mfma_kernels.hpp", "ks_kernels.hpp",
            "ks_launch.hpp", "gemm_kernels.hpp", "w4_device.hpp", "w4_launch.hpp", "w4_gemm.hpp",
-           "w4_mid.hpp", "w4_mid_launch.hpp", "w4_bwd.hpp", "w4_few.hpp", "w4_few_launch.hpp"]
+           "w4_mid.hpp", "w4_mid_launch.hpp", "w4_bwd.hpp", "w4_few.hpp", "w4_few_launch.hpp", "w4_plan.hpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

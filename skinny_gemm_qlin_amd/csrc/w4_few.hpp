@@ -55,6 +55,7 @@
 #pragma once
 #include "w4_device.hpp"
 #include "w4_launch.hpp"
+#include "w4_plan.hpp"
 
 namespace qlin {
 
@@ -69,26 +70,6 @@ struct W4FewParams {
     int groups;                       // K / group
     uint32_t ratio_magic;             // fold units per group r: unit / r = mulhi(unit, magic), 0: r = 1
 };
-
-// floats that an output's wave sums take: whole 16 bytes, not 16 of them so that rows start in different banks
-__host__ __device__ inline int w4_few_red(int nw) { return nw > 12 ? 20 : (nw + 3) / 4 * 4; }
-
-constexpr int kW4FewLoad = 512 + 8;  // elements that a 1 KB load of token rows takes: the next starts 16 bytes of banks on
-
-// Dynamic LDS: each wave's lines of the token rows, X of its fold units, scales and zero points as they are in
-// memory (from the 16-byte line their block starts in), the waves' sums.
-struct W4FewLds { uint32_t xsum, s, z, red, total; };
-
-__host__ __device__ inline W4FewLds w4_few_lds(int M, int U, int PL, int cols, int wrows, int groups, int nw) {
-    auto up = [](uint32_t b) { return (b + 15u) / 16u * 16u; };
-    W4FewLds o;
-    o.xsum = (uint32_t)(nw * ((PL * M + 1) / 2)) * kW4FewLoad * 2;
-    o.s = o.xsum + (uint32_t)nw * (PL * (128 / U)) * (M > 8 ? 128 : 64);
-    o.z = o.s + up((uint32_t)(wrows * groups * 2)) + 64;  // gated: two blocks, each with its own start and end
-    o.red = o.z + up((uint32_t)(wrows * groups)) + 64;
-    o.total = o.red + (uint32_t)(M * cols * w4_few_red(nw)) * 4;
-    return o;
-}
 
 template <int T, int U, int RM, int PL, int D, bool FULL>
 __global__ __launch_bounds__(1024) void w4_few_kernel(const W4FewParams p) {

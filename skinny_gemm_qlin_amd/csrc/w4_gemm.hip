@@ -31,39 +31,10 @@ hipError_t run(W4GemmParams p, int64_t c_first, int64_t c_count, int64_t splits,
     return hipGetLastError();
 }
 
-// Estimated time of the GEMM with square tiles.  A 64-deep step of a 256 x 256 tile takes 1.95 us (one workgroup a
-// compute unit), of a 128 x 128 tile 1.05 us alone on its unit and 1.2 to 1.4 us where two share one (2048 tokens,
-// 17408 x 5120, 80 steps: 544 large tiles 478 us, 2176 small ones 489 us; 509 tokens, 4096 x 7168, 112 steps: 32
-// large ones 203 us, 128 small ones 120 us; 256 tokens, 17408 x 5120, 272 small ones 120 us).
-float large_us(int64_t tiles, int64_t steps) { return (float)((tiles + 255) / 256 * steps) * 1.95f; }
-
-float small_us(int64_t tiles, int64_t steps) {
-    const int64_t full = tiles / 512, rest = tiles - full * 512;
-    return (float)steps * ((float)full * 1.22f + (rest == 0 ? 0.f : (rest <= 256 ? 1.05f : 1.4f)));
-}
-
-// Forward: `large` tile columns of 256 in large tiles, the rest in small ones.  Large tiles that would leave the
-// last of several rounds of workgroups part empty give their last columns to small tiles (2048 tokens: 17408 x 5120,
-// 2.1 rounds, 475 us in large tiles, 429 us so; 28672 x 4096 gated, 3.5 rounds, 532 and 521 us).
-struct GemmPlan { int64_t large; float us; };
-
-GemmPlan gemm_plan(int64_t M, int64_t cols, int64_t R) {
-    const int64_t steps = (R + 63) / 64, tm = (M + 255) / 256, tc = (cols + 255) / 256, tm2 = (M + 127) / 128;
-    GemmPlan o{0, 10.f + small_us(tm2 * ((cols + 127) / 128), steps)};
-    const float all = 10.f + large_us(tm * tc, steps);
-    if (all <= o.us) o = {tc, all};
-    const int64_t part = (tm * tc - 1) / 256 * 256 / tm;  // tile columns of all rounds but the last
-    if (part > 0) {
-        const float both = 15.f + large_us(tm * part, steps) + small_us(tm2 * ((cols - part * 256 + 127) / 128), steps);
-        if (both < o.us) o = {part, both};
-    }
-    return o;
-}
-
 template <int T, int EPI>
 hipError_t forward(const W4GemmParams& p, hipStream_t st) {
     constexpr int fold = EPI == kW4Store ? 1 : 2;  // rows of W a column of the output takes
-    const int64_t large = gemm_plan(p.M, fold * p.C, p.R).large * 256 / fold, first = large < p.C ? large : p.C;
+    const int64_t large = w4_gemm_plan(p.M, fold * p.C, p.R).large * 256 / fold, first = large < p.C ? large : p.C;
     if (first > 0) {
         const hipError_t e = run<T, false, EPI, 256, 256, 2, 4>(p, 0, first, 1, st);
         if (e != hipSuccess) return e;
@@ -84,13 +55,6 @@ hipError_t run_few(int dtype, W4FewParams p, const W4FewPlan& pl, hipStream_t st
     return dtype == kFp16 ? w4_few_fp16(p, pl, st) : w4_few_bf16(p, pl, st);
 }
 
-// The kernel for 17 to 64 tokens also takes longer batches, in blocks of 64, where the GEMM's tiles would leave
-// compute units idle (128 tokens, 4096 x 7168: 22 us against 102), and matrices of fewer than four scales, which
-// the GEMM loads four at a time.
-bool use_mid(int64_t M, const W4Weight& w, const W4MidPlan& pl) {
-    return w.N * (w.K / w.group) < 4 || pl.us < gemm_plan(M, w.N, w.K).us;
-}
-
 hipError_t run_mid(int dtype, W4MidParams p, const W4MidPlan& pl, hipStream_t st) {
     p.groups = (int)(p.w.K / p.w.group);
     p.ratio_magic = ratio_magic(p.w.group, 32);
@@ -108,7 +72,7 @@ hipError_t launch_gemv_w4(const W4LinearArgs& a, hipStream_t st) {
         return run_few(a.dtype, d, pl, st);
     }
     W4MidPlan mp;
-    if (w4_mid_plan(a.M, a.w.K, a.w.group, a.w.N, false, mp) && use_mid(a.M, a.w, mp)) {
+    if (w4_mid_plan(a.M, a.w.K, a.w.group, a.w.N, false, mp) && w4_use_mid(a.M, a.w.N, a.w.K, a.w.group, mp)) {
         W4MidParams d{};
         d.x = a.x; d.ldx = a.ldx; d.M = (int)a.M; d.w = a.w; d.C = a.w.N;
         d.bias = a.bias; d.y = a.y; d.ldy = a.ldy;
@@ -129,7 +93,7 @@ hipError_t launch_glu_w4(const W4GluArgs& a, hipStream_t st) {
         return run_few(a.dtype, d, pl, st);
     }
     W4MidPlan mp;
-    if (w4_mid_plan(a.M, a.w.K, a.w.group, a.I, true, mp) && use_mid(a.M, a.w, mp)) {
+    if (w4_mid_plan(a.M, a.w.K, a.w.group, a.I, true, mp) && w4_use_mid(a.M, a.w.N, a.w.K, a.w.group, mp)) {
         W4MidParams d{};
         d.x = a.x; d.ldx = a.ldx; d.M = (int)a.M; d.w = a.w; d.I = a.I; d.C = a.I;
         d.y = a.y; d.ldy = a.ldy; d.gu = a.gu; d.ldgu = a.ldgu; d.dy = a.dy; d.lddy = a.lddy; d.act = a.act;

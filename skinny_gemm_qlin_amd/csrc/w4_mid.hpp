@@ -25,6 +25,7 @@
 #pragma once
 #include "w4_device.hpp"
 #include "w4_launch.hpp"
+#include "w4_plan.hpp"
 
 namespace qlin {
 
@@ -37,17 +38,6 @@ struct W4MidParams {
     int groups;                       // K / group
     uint32_t ratio_magic;             // 32-K chunks per group r: chunk / r = mulhi(chunk, magic), 0: r = 1
 };
-
-constexpr int kW4MidStep = 256;
-
-constexpr int w4_mid_stage(int XR, int NTL) { return (XR * 2 + NTL * 16) * kW4MidStep; }
-// tokens whose sums are added at a time: the waves' sums take the first stage's LDS
-constexpr int w4_mid_parts(int NTL) { return NTL > 1 ? 8 : 16; }
-
-// scales and zero points of the workgroup's rows, as in memory from the 16-byte line each block starts in
-inline __host__ __device__ uint32_t w4_mid_scales(int rows, int groups) {
-    return ((uint32_t)(rows * groups * 2) + 15u) / 16u * 16u + ((uint32_t)(rows * groups) + 15u) / 16u * 16u + 128u;
-}
 
 template <int T, int XR, int NTL, int STAGES>  // XR: token rows staged, 32, 48 or 64; 2 <= STAGES <= 4
 __global__ __launch_bounds__(512) void w4_mid_kernel(const W4MidParams p) {
