@@ -18,6 +18,9 @@ hipError_t run(const W4MidParams& p, const W4MidPlan& pl, hipStream_t st) {
 template <int T, int XR, int NTL>
 hipError_t stages(const W4MidParams& p, const W4MidPlan& pl, hipStream_t st) {
     constexpr int most = w4_mid_most_stages(XR, NTL);
+    if constexpr (NTL == 1) {
+        if (pl.stages == 2) return run<T, XR, NTL, 2>(p, pl, st);
+    }
     return pl.stages == most ? run<T, XR, NTL, most>(p, pl, st) : run<T, XR, NTL, most - 1>(p, pl, st);
 }
 

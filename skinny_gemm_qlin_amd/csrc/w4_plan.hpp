@@ -91,7 +91,9 @@ constexpr uint32_t w4_mid_scales(int rows, int groups) {
 constexpr uint32_t w4_mid_fixed_lds(int xr, int ntl, int stages) { return stages * w4_mid_stage(xr, ntl) + 256; }
 
 // Stages: as many as leave 16 KB for scales, or one less where the scales take more.  A step's loads come back
-// later than a step takes (48 tokens, 4096 x 7168, one row tile: two stages 28.8 us, three 22.4).
+// later than a step takes (48 tokens, 4096 x 7168, one row tile: two stages 28.8 us, three 22.4), so two, which
+// one row tile goes down to, are for rows of more scales than fit next to three (64 tokens, 8192 rows, groups of 32:
+// K = 17600, three stages, 55 us; K = 17632, two, 71 us, in the GEMM 302; K = 28672 107 us, in the GEMM 464).
 constexpr int w4_mid_most_stages(int xr, int ntl) { return 4 * w4_mid_stage(xr, ntl) <= 144 * 1024 ? 4 : 3; }
 
 struct W4MidPlan { int ntl, stages; uint32_t scales; float us; };  // row tiles, LDS of the scales, estimated time
@@ -108,10 +110,12 @@ inline bool w4_mid_plan(int64_t M, int64_t K, int64_t group, int64_t C, bool glu
     for (int ntl = 1; ntl <= 4; ++ntl) {
         const uint32_t scales = w4_mid_scales(32 * ntl, (int)groups);
         int stages = w4_mid_most_stages(xr, ntl);
-        if (w4_mid_fixed_lds(xr, ntl, stages) + scales > kW4LdsBytes) --stages;
+        const int least = ntl == 1 ? 2 : stages - 1;
+        while (stages > least && w4_mid_fixed_lds(xr, ntl, stages) + scales > kW4LdsBytes) --stages;
         if (w4_mid_fixed_lds(xr, ntl, stages) + scales > kW4LdsBytes) break;
         const int64_t wgs = ((rows + 32 * ntl - 1) / (32 * ntl)) * ((M + 63) / 64);
-        const float us = 6.f + (float)((wgs + 255) / 256 * ((K + 255) / 256)) * (M <= 32 ? 0.27f + 0.29f * ntl : 0.25f + 0.4f * ntl);
+        const float step = (M <= 32 ? 0.27f + 0.29f * ntl : 0.25f + 0.4f * ntl) * (ntl == 1 && stages == 2 ? 1.3f : 1.f);
+        const float us = 6.f + (float)((wgs + 255) / 256 * ((K + 255) / 256)) * step;
         if (o.ntl > 0 && us >= o.us) continue;
         o.us = us;
         o.ntl = ntl;

@@ -80,3 +80,22 @@ def test_more_gates_than_a_launch_has_threads(ql):
     got = dgu[rows].double()
     assert bool(((got - want).abs() <= want.abs() * 2.0 ** -8 + slack).all())
     assert torch.equal(buf[:, 2 * I:], pads)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("M,N,groups", [(64, 100, 551), (50, 33, 896), (64, 70, 935), (64, 65, 936), (48, 41, 810),
+                                        (33, 64, 1100), (20, 100, 1270), (200, 70, 700)])
+def test_rows_of_many_scales(ql, M, N, groups, dtype):
+    """17 and more tokens, groups of 32: two stages next to the scales of 32 rows, on each side of the limits."""
+    K = 32 * groups
+    w, ws, wz = gen_w4(N, K, 32, dtype, True, seed=N, exact_scales=True)
+    layer = dev_w(w, ws, wz)
+    W, P = ref.dense(w, f64(ws), wz, 32), ref.dense_parts(w, f64(ws), wz, 32)
+    x = gen_x(M, K, dtype, seed=M, scale=0.1)
+    y, S, Q = ref.product(f64(x), W.T, P.T)
+    E = ref.sum_tolerance(S, Q, K, dtype, True)
+    close(ql.qlin_gemv_w4(x.cuda(), *layer), y, ref.rounded_tolerance(y, E, dtype), "y")
+    if N % 2 == 0:
+        gu = torch.empty((M, N), dtype=DT[dtype], device="cuda")
+        ql.qlin_glu_w4(x.cuda(), *layer, gu=gu)
+        close(gu, y, ref.rounded_tolerance(y, E, dtype), "gu")

@@ -27,3 +27,28 @@ def test_kernels_by_size(plan):
                                (64, 5120, 128, 17408, False), (128, 7168, 128, 4096, False), (2048, 5120, 128, 17408, False),
                                (2048, 4096, 128, 14336, True)])]
     assert got == ["few", "few", "mid", "mid", "mid", "gemm", "gemm"]
+
+
+def _mid_lds(tokens, ntl, stages, groups):
+    """LDS of the mid kernel: stages of 256 K of its token and code rows, the scales of 32 ntl rows."""
+    rows = 32 if tokens <= 32 else 48 if tokens <= 48 else 64
+    return stages * (rows * 512 + ntl * 32 * 128) + 256 + 3 * 32 * ntl * groups + 128
+
+
+@pytest.mark.parametrize("M", [17, 32, 33, 48, 49, 64])
+def test_many_scales_keep_the_mid_kernel(plan, M):
+    """17 to 64 tokens: as many stages as fit next to the scales, down to two, before the GEMM takes the call."""
+    groups = list(range(400, 1400, 4))
+    got = plan([(M, 32 * g, 32, 8192, False) for g in groups])
+    seen = set()
+    for g, p in zip(groups, got):
+        if _mid_lds(M, 1, 2, g) <= 160 * 1024:
+            assert p[0] == "mid", (g, p)
+            seen.add(p[2])
+            assert _mid_lds(M, p[1], p[2], g) <= 160 * 1024
+            if p[2] == 2:  # only where three do not fit
+                assert p[1] == 1 and _mid_lds(M, 1, 3, g) > 160 * 1024
+        elif p[0] == "mid":
+            raise AssertionError((g, p))
+    assert 2 in seen and 3 in seen
+    assert plan([(64, 28672, 32, 8192, False)])[0][:3] == ["mid", 1, 2]  # a down projection in groups of 32
