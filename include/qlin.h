@@ -386,9 +386,11 @@ enum {
 /* y[m,n] = r16( sum_k x[m,k] * W[n,k] + bias[n] ), one rounding.
  *   x 16-bit [M, ldx] (16-byte aligned, ldx % 8 == 0); bias 16-bit [N] or
  *   NULL; y 16-bit [M, ldy].
- * Up to 16 tokens (and 10240 groups a row) the scales multiply fp32 sums of
- * code * x and of zero * x, and nothing else rounds; above, a weight is rounded
- * once to dtype before it is multiplied.  A token that holds an infinity or a
+ * Up to 16 tokens the scales multiply fp32 sums of code * x and of zero * x,
+ * and nothing else rounds, for rows of at most 5300 groups (1 to 8 tokens) or
+ * 2600 (9 to 16); for the gated front below, 2600 and 1290.  Rows of more
+ * groups may be taken, and more tokens are, with every weight rounded once to
+ * dtype before it is multiplied.  A token that holds an infinity or a
  * NaN gives a row of infinities and NaNs (of 16-bit floats above 2^120, where
  * those fp32 sums overflow, too); other tokens' rows are not touched by it. */
 int qlin_gemv_w4(const void* x, int64_t ldx, int64_t M, int64_t K, int dtype,

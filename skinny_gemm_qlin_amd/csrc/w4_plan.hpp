@@ -33,15 +33,16 @@ constexpr W4FewLds w4_few_lds(int M, int U, int PL, int cols, int wrows, int gro
 
 constexpr int kW4FewMaxM = 16;
 
-// How a call is laid out; false if its token rows and scales do not fit LDS
-// even one tile of rows at a time.
+// How a call is laid out; false if its token rows and the scales of one tile
+// of rows do not fit LDS.  They do up to 5300 groups a row for 1 to 8 tokens
+// and 2600 for 9 to 16 (the worst of all sizes; tiles of 16 rows), gated 2600
+// and 1290 (two tiles): the rows for which qlin.h promises unrounded weights.
 struct W4FewPlan { int pl, nw, passes, rows, depth; uint32_t lds; };
 
 inline bool w4_few_plan(int64_t M, int64_t K, int64_t group, int64_t C, bool glu, W4FewPlan& o) {
     if (M > kW4FewMaxM) return false;
     const int U = group % 128 == 0 ? 128 : (group % 64 == 0 ? 64 : 32);
     const int64_t lines = (K + 255) / 256, groups = K / group;
-    if (groups > kW4LdsBytes / 16) return false;
     // one line a wave on short rows: more waves to hide latency (1024 x 1024: 3.3 us, two lines 3.4)
     // 9 to 16 tokens: one, or the two halves' operands would not fit the registers
     const bool full = M > 8;
@@ -51,8 +52,11 @@ inline bool w4_few_plan(int64_t M, int64_t K, int64_t group, int64_t C, bool glu
     // 8 columns each.  Where LDS does not hold a share, K is first walked in up to four times as many passes, then
     // the shares get smaller and the rounds of workgroups more.
     const int64_t least = (lines + 16 * o.pl - 1) / (16 * o.pl);
-    for (int64_t rounds = 1;; ++rounds) {
-        bool smallest = true;
+    const int64_t fewest = (lines + 4 * least * o.pl - 1) / (4 * least * o.pl), tile = TR * (glu ? 2 : 1);
+    if (tile * groups >= kW4LdsBytes ||
+        w4_few_lds((int)M, U, o.pl, glu ? 16 : 8, (int)tile, (int)groups, (int)fewest).total > kW4LdsBytes)
+        return false;
+    for (int64_t rounds = 1;; ++rounds) {  // ends at the latest with 8 columns and the fewest waves
         for (int64_t passes = least; passes <= 4 * least; ++passes) {
             o.nw = (int)((lines + passes * o.pl - 1) / (passes * o.pl));
             o.passes = (int)((lines + o.nw * o.pl - 1) / (o.nw * o.pl));
@@ -60,7 +64,6 @@ inline bool w4_few_plan(int64_t M, int64_t K, int64_t group, int64_t C, bool glu
                 const int64_t wgs = 256 * per_cu * rounds;
                 int64_t rows = (C + wgs - 1) / wgs;
                 if (rows < 8) rows = 8;
-                smallest = smallest && rows == 8;
                 const int64_t wrows = (rows + TR - 1) / TR * TR * (glu ? 2 : 1);
                 if (wrows >= 4096 || wrows * groups >= kW4LdsBytes) continue;
                 o.rows = (int)rows;
@@ -72,7 +75,6 @@ inline bool w4_few_plan(int64_t M, int64_t K, int64_t group, int64_t C, bool glu
                 return true;
             }
         }
-        if (smallest) return false;
     }
 }
 

@@ -90,6 +90,23 @@ def test_more_tokens_round_each_weight_once(ql, M, dtype, gated):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("M,groups,gated", [(1, 5300, False), (8, 5300, False), (9, 2600, False), (16, 2600, False),
+                                            (1, 2600, True), (8, 2600, True), (9, 1290, True), (16, 1290, True)])
+def test_longest_rows_without_rounding(ql, M, groups, gated, dtype):
+    """The most groups a row that the header names."""
+    _check(ql, M, 24, 32 * groups, 32, dtype, M % 2 == 0, False, gated)
+    _check(ql, M, 24, 64 * groups, 64, dtype, True, False, gated)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("M,groups,gated", [(1, 6700, False), (8, 5400, False), (9, 2960, False), (16, 2680, False),
+                                            (1, 3320, True), (8, 2680, True), (9, 1470, True), (16, 1320, True)])
+def test_longer_rows_round(ql, M, groups, gated, dtype):
+    """Rows of more scales than the decode kernels hold: each weight is rounded once."""
+    _check(ql, M, 24, 32 * groups, 32, dtype, True, True, gated)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("M", [1, 16, 17, 33, 64, 65, 300, 700])
 def test_gradient_rounds_each_weight_once(ql, M, dtype):
     rng = np.random.default_rng(M)

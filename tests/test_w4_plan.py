@@ -52,3 +52,29 @@ def test_many_scales_keep_the_mid_kernel(plan, M):
             raise AssertionError((g, p))
     assert 2 in seen and 3 in seen
     assert plan([(64, 28672, 32, 8192, False)])[0][:3] == ["mid", 1, 2]  # a down projection in groups of 32
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_rows_that_decode_without_rounding(plan, gated):
+    """The decode kernels take rows of as many groups as the header promises unrounded weights for."""
+    calls, want = [], []
+    for M in range(1, 17):
+        most = (2600 if M <= 8 else 1290) if gated else (5300 if M <= 8 else 2600)
+        for group in (32, 64, 96, 128, 192, 384):
+            for groups in (most, most - 1, most - 77, most // 2):
+                if group * groups <= 1 << 20:
+                    calls += [(M, group * groups, group, C, gated) for C in (1, 500, 20000)]
+    assert all(p[0] == "few" for p in plan(calls))
+    # far past it they cannot: the scales of one tile fill LDS
+    assert all(p[0] != "few" for p in plan([(M, 32 * 7000, 32, 500, gated) for M in range(1, 17)]))
+
+
+def test_layouts_fit(plan):
+    """What a decode call is given fits LDS, its waves a workgroup and its passes the row."""
+    calls = [(M, group * groups, group, C, gated) for M in (1, 2, 5, 8, 9, 12, 16) for group in (32, 128, 160)
+             for groups in (1, 3, 40, 41, 300, 1200) for C in (1, 9, 4099, 17408, 300000) for gated in (False, True)]
+    for (M, K, group, C, gated), p in zip(calls, plan(calls)):
+        assert p[0] == "few"
+        _, pl, nw, passes, rows, depth, lds = p
+        assert 1 <= nw <= 16 and pl in (1, 2) and depth in (1, 2) and lds <= 160 * 1024 and rows >= 8
+        assert nw * pl * passes * 256 >= K > nw * pl * (passes - 1) * 256
