@@ -45,13 +45,18 @@
 //   barrier, which leaves the weight loads outstanding; its own lines of the
 //   token rows by each wave, without a barrier, so that waves walk a long row
 //   independently (with a barrier a pass and all tokens' slice shared: 14336 x
-//   4099, 5 tokens 19.6 us, now 17.4).  The waves' sums are added in wave order
+//   4099, 5 tokens 19.6 us, now 17.1).  The waves' sums are added in wave order
 //   through LDS (deterministic, no workspace).  Rows longer than 16 waves'
 //   lines (K > 8192 or 4096), or too long for LDS, are walked in passes.
 //
+// Nothing may be in private memory here: its loads return in order behind the
+// weights' and would be waited for with them (the offsets of the scales in an
+// array of private memory cost a call 1 to 2 us).
+//
 // Measured (bf16, zero points, groups of 128, weights cold): 17408 x 5120, one
-// token 13.1 us (3.6 TB/s of codes and scales), 8 tokens 15.0, 16 tokens 17.9;
-// 28672 x 4096 gated, one token 14.9 us (4.1 TB/s); 1024 x 1024 3.8 us.
+// token 11.6 us (4.0 TB/s of codes and scales), 8 tokens 13.1, 16 tokens 15.8;
+// 28672 x 4096 gated, one token 13.8 us (4.4 TB/s), 16 tokens 18.0; 1024 x 1024
+// 3.6 us.
 #pragma once
 #include "w4_device.hpp"
 #include "w4_launch.hpp"
@@ -126,7 +131,9 @@ __global__ __launch_bounds__(1024) void w4_few_kernel(const W4FewParams p) {
     uint32_t sat[2], zat[2];  // LDS offsets of the gate and the up block (plain: the first)
     {
         uint32_t so = at.s, zo = at.z;
-        for (int part = 0; part < parts; ++part) {
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {  // a trip count known here keeps the offsets in registers
+            if (part == 1 && !glu) break;
             const int64_t first = (c0 + (part ? p.I : 0)) * G;
             const uint32_t count = (uint32_t)CT * G;
             const uintptr_t sa = (uintptr_t)(p.w.ws + first), za = (uintptr_t)(p.w.wz + (has_z ? first : 0));

@@ -14,7 +14,12 @@ hipError_t w4_few_run(const W4FewParams& p, const W4FewPlan& pl, hipStream_t st)
 
 template <int T, int U, int RM, int PL, bool FULL>
 hipError_t w4_few_d(const W4FewParams& p, const W4FewPlan& pl, hipStream_t st) {
-    return pl.depth == 1 ? w4_few_run<T, U, RM, PL, 1, FULL>(p, pl, st) : w4_few_run<T, U, RM, PL, 2, FULL>(p, pl, st);
+    if constexpr (FULL && U == 32) {
+        return w4_few_run<T, U, RM, PL, 1, FULL>(p, pl, st);
+    } else {
+        return pl.depth == 1 ? w4_few_run<T, U, RM, PL, 1, FULL>(p, pl, st)
+                             : w4_few_run<T, U, RM, PL, 2, FULL>(p, pl, st);
+    }
 }
 
 template <int T, int U, int RM>

@@ -69,9 +69,11 @@ inline bool w4_few_plan(int64_t M, int64_t K, int64_t group, int64_t C, bool glu
                 o.rows = (int)rows;
                 o.lds = w4_few_lds((int)M, U, o.pl, (int)rows * (glu ? 2 : 1), (int)wrows, (int)groups, o.nw).total;
                 if (o.lds * per_cu > kW4LdsBytes && !(rows == 8 && o.lds <= kW4LdsBytes)) continue;
-                // about 20 to 32 KB a compute unit in flight (17408 x 5120, 10 waves: one tile ahead 11.2 us,
-                // two 11.8; 28672 x 4096 gated, 8 waves: 14.9 and 13.1)
-                o.depth = o.nw * o.pl * (full ? 2 : 1) > 16 ? 1 : 2;
+                // about 20 to 32 KB a compute unit in flight (17408 x 5120, 10 waves of two lines: one tile ahead
+                // 11.5 us, two 11.4; 28672 x 4096 gated, 8 waves: 15.4 and 14.0).  Two tiles of 16 rows ahead do
+                // not fit the registers with folds of 32 (16 tokens, 4096 x 4096, groups of 32: 8.9 and 11.9 us;
+                // 9 tokens 8.0 and 10.1)
+                o.depth = o.nw * o.pl * (full ? 2 : 1) > 16 || (full && U == 32) ? 1 : 2;
                 return true;
             }
         }
