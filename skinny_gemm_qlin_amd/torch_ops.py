@@ -182,11 +182,13 @@ def _(x, wr, w13, s13, w2, s2, topk, alpha=1.0, limit=10.0):
 
 # ----------------------------------------------------------------------------- 4-bit weights with group scales
 
-def _rows8(t: torch.Tensor) -> torch.Tensor:
-    """A gradient as the kernels read it: rows of unit stride, 16-byte aligned, a pitch that is a multiple
-    of 8.  Autograd also hands out expanded and transposed gradients; those are copied."""
+def _rows(t: torch.Tensor, multiple: int) -> torch.Tensor:
+    """A gradient as the kernels read it: rows of unit stride, for a matrix product (multiple 8) 16-byte aligned
+    with a pitch that is a multiple of 8, for the gates (multiple 1) any.  Autograd also hands out expanded and
+    transposed gradients; those are copied."""
     rows, cols = t.shape
-    if t.stride(1) == 1 and t.data_ptr() % 16 == 0 and (rows == 1 or (t.stride(0) % 8 == 0 and t.stride(0) >= cols)):
+    if (t.stride(1) == 1 and t.data_ptr() % (2 * multiple) == 0
+            and (rows == 1 or (t.stride(0) % multiple == 0 and t.stride(0) >= cols))):
         return t
     out = t.new_empty((rows, (cols + 7) // 8 * 8))[:, :cols]
     out.copy_(t)
@@ -214,7 +216,7 @@ def _(x, w, ws, wz=None, bias=None):
 def gemv_w4_bwd(dy: torch.Tensor, w: torch.Tensor, ws: torch.Tensor, wz: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Input gradient dx [M, K] of gemv_w4 from dy [M, N] in any layout."""
     hits["gemv_w4_bwd"] += 1
-    return qlin_gemv_w4_bwd(_rows8(dy), w, ws, wz)
+    return qlin_gemv_w4_bwd(_rows(dy, 8), w, ws, wz)
 
 
 @gemv_w4_bwd.register_fake
@@ -260,7 +262,7 @@ def glu_w4_bwd(dy: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor, z13: Opti
                act: int = 0) -> Tuple[torch.Tensor, torch.Tensor]:
     """(dx [M, K], dgu [M, 2I]) of glu_w4 from dy [M, I] in any layout and gu or x."""
     hits["glu_w4_bwd"] += 1
-    return qlin_glu_w4_bwd(_rows8(dy), w13, s13, z13, act=act, x=x, gu=gu)
+    return qlin_glu_w4_bwd(_rows(dy, 1), w13, s13, z13, act=act, x=x, gu=gu)
 
 
 @glu_w4_bwd.register_fake
