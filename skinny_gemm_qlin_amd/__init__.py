@@ -419,21 +419,22 @@ _U8_ONLY = torch.uint8
 
 def _w4_weight(a, name, w, ws, wz):
     """Checks a 4-bit weight against the 16-bit operand `a`; returns (N, K, group, dtype flag, device index)."""
-    dt = _DT16.get(a.dtype)
-    if dt is not None and w.dim() == 2 and ws.dim() == 2 and a.dim() == 2:
-        N, Kh = w.shape
-        rows, groups = ws.shape
-        K, dev = 2 * Kh, a.get_device()
-        if (rows == N and groups > 0 and K % groups == 0 and w.dtype is _U8_ONLY and ws.dtype is a.dtype
-                and ws.is_contiguous() and w.get_device() == dev == ws.get_device() and dev >= 0
-                and (w.stride(1) == 1 or Kh == 1) and (a.stride(1) == 1 or a.shape[1] == 1)
-                and (wz is None or (wz.dtype is _U8_ONLY and wz.shape == ws.shape and wz.is_contiguous()
-                                    and wz.get_device() == dev))):
-            return N, K, K // groups, dt, dev
+    try:
+        dt = _DT16.get(a.dtype)
+        if dt is not None and w.dim() == 2 and ws.dim() == 2 and a.dim() == 2:
+            N, Kh = w.shape
+            rows, groups = ws.shape
+            K, dev = 2 * Kh, a.get_device()
+            if (rows == N and groups > 0 and K % groups == 0 and w.dtype is _U8_ONLY and ws.dtype is a.dtype
+                    and ws.is_contiguous() and w.get_device() == dev == ws.get_device() and dev >= 0
+                    and (w.stride(1) == 1 or Kh == 1) and (a.stride(1) == 1 or a.shape[1] == 1)
+                    and (wz is None or (wz.dtype is _U8_ONLY and wz.shape == ws.shape and wz.is_contiguous()
+                                        and wz.get_device() == dev))):
+                return N, K, K // groups, dt, dev
+    except AttributeError:  # something here is no tensor
+        pass
     # something is wrong: say what
-    if dt is None:
-        raise TypeError(f"{name}: dtype {a.dtype} not in {tuple(_DT16)}")
-    _need(a, name, (a.dtype,), 2)
+    _need(a, name, tuple(_DT16), 2)
     _need(w, "w", (torch.uint8,), 2)
     _need(ws, "ws", (a.dtype,), 2)
     N, Kh = w.shape
@@ -450,8 +451,8 @@ def _out16(t, name, like, rows, cols, stream=None):
     """An operand or output of `like`'s type and device: allocated if None, or checked."""
     if t is None:
         return _own(name, (rows, cols), like.dtype, like, stream)
-    if (t.dtype is like.dtype and t.dim() == 2 and t.shape[0] == rows and t.shape[1] == cols
-            and (t.stride(1) == 1 or cols == 1) and t.get_device() == like.get_device()):
+    if (isinstance(t, torch.Tensor) and t.dtype is like.dtype and t.dim() == 2
+            and t.shape[0] == rows and t.shape[1] == cols and (t.stride(1) == 1 or cols == 1) and t.get_device() == like.get_device()):
         return t
     _need(t, name, (like.dtype,), 2)
     raise ValueError(f"{name} must be [{rows}, {cols}] on {like.device}, got {tuple(t.shape)} on {t.device}")
@@ -512,6 +513,8 @@ def _w4_workspace(workspace, M, N, K, like, stream):
         if not need:
             return None, 0
         workspace = _own("a workspace", (need,), torch.uint8, like, stream)
+    elif not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace: expected a torch.Tensor")
     elif workspace.get_device() != like.get_device() or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on {like.device}")
     return workspace, workspace.numel() * workspace.element_size()
