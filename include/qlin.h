@@ -372,7 +372,9 @@ int qlin_moe_ffn_mxfp4(const void* x, int64_t ldx, int64_t M, int64_t H,
  * line that an end of the array lies in may be read besides.)
  * dtype is the type of every 16-bit operand and result of the call.
  * Requires K % 32 == 0, 32 <= K <= 2^20, G >= 32, G % 32 == 0, K % G == 0,
- * 1 <= N <= 2^20, 1 <= M <= QLIN_MAX_M_PREFILL.  All sums are fp32.  The
+ * 1 <= N <= 2^20, 1 <= M <= QLIN_MAX_M_PREFILL.  All sums are fp32.  Where a
+ * call rounds its weights to dtype, an fp16 one beyond 65504 is an infinity; of
+ * bf16 scales above 2^124 in absolute value zero * ws may be one.  The
  * weights are frozen: there is no gradient of codes, scales or zero points. */
 enum {
     QLIN_DT_BF16 = 0,

@@ -99,3 +99,33 @@ def test_rows_of_many_scales(ql, M, N, groups, dtype):
         gu = torch.empty((M, N), dtype=DT[dtype], device="cuda")
         ql.qlin_glu_w4(x.cuda(), *layer, gu=gu)
         close(gu, y, ref.rounded_tolerance(y, E, dtype), "gu")
+
+
+def _one_weight(rows, dtype, code, zero, scale):
+    """A layer whose weights are all scale * (code - zero)."""
+    w = torch.full((rows, 32), code * 17, dtype=torch.uint8, device="cuda")
+    ws = torch.full((rows, 2), scale, dtype=DT[dtype], device="cuda")
+    return w, ws, torch.full((rows, 2), zero, dtype=torch.uint8, device="cuda")
+
+
+@pytest.mark.parametrize("M", [1, 9, 16, 17, 40, 300])
+def test_weights_beyond_fp16(ql, M):
+    """8000 * 15 is no fp16 number: without rounding a product of it is finite, with it infinite."""
+    layer = _one_weight(72, "fp16", 15, 0, 8000.0)
+    x = torch.full((M, 64), 2.0 ** -10, dtype=torch.float16, device="cuda")
+    y = ql.qlin_gemv_w4(x, *layer)
+    assert bool((y == (7500.0 if M <= 16 else float("inf"))).all())
+    dx = ql.qlin_gemv_w4_bwd(torch.full((M, 72), 2.0 ** -10, dtype=torch.float16, device="cuda"), *layer)
+    assert bool(torch.isinf(dx).all())
+
+
+@pytest.mark.parametrize("M", [1, 9, 16, 17, 40, 300])
+@pytest.mark.parametrize("code,zero", [(15, 0), (0, 15), (9, 8), (14, 15)])
+def test_largest_bf16_scales(ql, M, code, zero):
+    """Scales of 2^124: exact products with small activations, though zero * scale is close to fp32's end."""
+    layer = _one_weight(72, "bf16", code, zero, 2.0 ** 124)
+    x = torch.full((M, 64), 2.0 ** -100, dtype=torch.bfloat16, device="cuda")
+    y = ql.qlin_gemv_w4(x, *layer)
+    assert bool((y == (code - zero) * 2.0 ** 30).all())  # 64 * 2^124 * 2^-100
+    dx = ql.qlin_gemv_w4_bwd(torch.full((M, 72), 2.0 ** -100, dtype=torch.bfloat16, device="cuda"), *layer)
+    assert bool((dx == (code - zero) * 9 * 2.0 ** 27).all())
