@@ -242,7 +242,8 @@ gemv_w4.register_autograd(_gemv_w4_grad, setup_context=_gemv_w4_setup)
 def glu_w4(x: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor, z13: Optional[torch.Tensor] = None, act: int = 0,
            keep: bool = False) -> Tuple[torch.Tensor, torch.Tensor]:
     """Gated feed-forward front -> (y [M, I], gu).  keep: gu [M, 2I] holds gate and up
-    for the backward pass; otherwise gu is empty and they are recomputed from x."""
+    for the backward pass and has no gradient of its own (a compiled function that returns it
+    would ask for one); otherwise gu is empty and they are recomputed from x."""
     hits["glu_w4"] += 1
     gu = x.new_empty((x.shape[0], (w13.shape[0] + 7) // 8 * 8))[:, :w13.shape[0]] if keep else None
     y = qlin_glu_w4(x, w13, s13, z13, act=act, gu=gu)
@@ -283,7 +284,7 @@ def _glu_w4_setup(ctx, inputs, output):
 
 def _glu_w4_grad(ctx, dy, dgu):
     kept, w13, s13, z13 = ctx.saved_tensors
-    if dgu is not None:
+    if dgu is not None and dgu.numel():  # a compiled function that returns both outputs has one for an empty gu, too
         raise RuntimeError("glu_w4: gu is kept for the backward pass and has no gradient of its own")
     if dy is None:
         return None, None, None, None, None, None
