@@ -1,10 +1,11 @@
 // w4_bwd.hpp -- input gradient dx = dy W of the 4-bit layer for up to 64
 // tokens (the GEMM takes more).
 //
-// Bound: the weights' stream (K/2 bytes a row), and close behind it the vector
-// unit: the scale varies along the reduction, so a weight is dequantised
-// before it is multiplied, (code - zero) * s in fp32 rounded once to the 16-bit
-// type, 2.8 instructions a code.
+// Bound: the latency of the weights' stream (K/2 bytes a row): four waves a
+// compute unit, each a block ahead.  Behind it the vector unit: the scale
+// varies along the reduction, so a weight is dequantised before it is
+// multiplied, (code - zero) * s in fp32 rounded once to the 16-bit type, 2.8
+// instructions a code (5120 x 5120, 7 tokens: busy for 4 of 9.4 us).
 //
 // A B operand of v_mfma_f32_16x16x32 wants 8 successive n of one column k in a
 // lane.  Lane (c = lane % 16, q = lane / 16) loads CW codes of row 8q + j for j

@@ -22,9 +22,10 @@
 //
 // * 7 instructions per 8 codes: two masks, a shift and four converts, for any
 //   number of tokens (the vector unit is the second bound: about 5 us of its
-//   time for 17408 x 5120).  Scales stay out of the products: with D = sum
-//   code * x and X = sum x over a group, y = sum s * D - sum (s * zero) * X,
-//   exact in code * x, fp32 sums, no rounding of weights.  The second sum is a
+//   time for 17408 x 5120, 7 to 8 us with the exchange of 9 to 16 tokens).
+//   Scales stay out of the products: with D = sum code * x and X = sum x over a
+//   group, y = sum s * D - sum (s * zero) * X, exact in code * x, fp32 sums, no
+//   rounding of weights.  The second sum is a
 //   product of its own, four groups at a time on v_mfma_f32_16x16x4_f32; X is
 //   what the tokens' products with a B operand of ones give, found while the
 //   weights are still in flight.  Groups that are no multiple of 128 (fold unit
@@ -45,7 +46,7 @@
 //   barrier, which leaves the weight loads outstanding; its own lines of the
 //   token rows by each wave, without a barrier, so that waves walk a long row
 //   independently (with a barrier a pass and all tokens' slice shared: 14336 x
-//   4099, 5 tokens 19.6 us, now 17.1).  The waves' sums are added in wave order
+//   4099, 5 tokens 19.6 us, now 16.3).  The waves' sums are added in wave order
 //   through LDS (deterministic, no workspace).  Rows longer than 16 waves'
 //   lines (K > 8192 or 4096), or too long for LDS, are walked in passes.
 //
@@ -54,8 +55,8 @@
 // array of private memory cost a call 1 to 2 us).
 //
 // Measured (bf16, zero points, groups of 128, weights cold): 17408 x 5120, one
-// token 11.6 us (4.0 TB/s of codes and scales), 8 tokens 13.1, 16 tokens 15.8;
-// 28672 x 4096 gated, one token 13.8 us (4.4 TB/s), 16 tokens 18.0; 1024 x 1024
+// token 11.5 us (4.1 TB/s of codes and scales), 8 tokens 13.5, 16 tokens 16.1;
+// 28672 x 4096 gated, one token 13.9 us (4.4 TB/s), 16 tokens 19.0; 1024 x 1024
 // 3.6 us.
 #pragma once
 #include "w4_device.hpp"

@@ -6,7 +6,7 @@
 // workgroup reads all of x, M K 2 bytes), and the vector unit's dequantisation
 // come out within a factor of two of each other; so a workgroup owns 32 to 128
 // weight rows (gated: half of them gate, half up) for all tokens, the x of a
-// step is shared in LDS, and no weight is dequantised twice.
+// step is shared in LDS, and a weight is dequantised once for 64 tokens.
 //
 // A step is 256 K: codes of BN rows (one 128-byte line each) and x of BM tokens
 // go straight to LDS (global_load_lds, XOR-swizzled slots), STAGES - 1 steps
@@ -18,10 +18,11 @@
 // waves' sums are added in wave order through the first stage's LDS at the
 // end, 16 or 8 tokens at a time.
 //
-// Measured (weights cold): 48 tokens, 4096 x 4096 14.3 us, 8192 x 8192 27.2,
-// 2 x 2051 x 7168 gated 21.4; 64 tokens, 17408 x 5120 36.9 us.  With few rows
-// half the compute units are idle, and a step takes what its token rows take
-// to arrive: 0.36 us with 32 of them, 0.5 with 48, 0.6 with 64.
+// Measured (weights cold): 48 tokens, 4096 x 4096 14.0 us, 8192 x 8192 29.5,
+// 2 x 2051 x 7168 gated 21.2; 64 tokens, 17408 x 5120 36.9 us (the vector unit
+// busy for 14 of them, the matrix cores for 5); 509 tokens, 4096 x 7168 57 us.
+// With few rows half the compute units are idle, and a step takes what its
+// token rows take to arrive: 0.36 us with 32 of them, 0.5 with 48, 0.6 with 64.
 #pragma once
 #include "w4_device.hpp"
 #include "w4_launch.hpp"
