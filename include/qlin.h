@@ -436,9 +436,11 @@ int qlin_glu_w4(const void* x, int64_t ldx, int64_t M, int64_t K, int dtype,
  * are otherwise recomputed from x in fp32 by the forward kernel.  dgu (the
  * gradient of [g, u], the left operand of dx) is always written: 16-byte
  * aligned, lddgu >= 2I, lddgu % 8 == 0, every row readable up to the next
- * multiple of 8 after 2I; it may be gu itself.  An infinite gate, as fp16 keeps
- * one beyond its range, has act(-inf) = act'(-inf) = 0 and act'(inf) = 1.  dx
- * may be NULL (not computed).  workspace as in qlin_gemv_w4_bwd with N = 2I. */
+ * multiple of 8 after 2I; it may be gu itself, at gu's pitch, and otherwise
+ * overlaps no input.  An infinite gate, as fp16 keeps one beyond its range, has
+ * act(-inf) = act'(-inf) = 0 and act'(inf) = 1; an infinite u gives infinities
+ * and NaNs.  dx, which overlaps no other operand, may be NULL (not computed).
+ * workspace as in qlin_gemv_w4_bwd with N = 2I. */
 int qlin_glu_w4_bwd(const void* dy, int64_t lddy, int64_t M, int64_t I, int dtype, int act,
                     const void* x, int64_t ldx, const void* gu, int64_t ldgu,
                     const uint8_t* w13, int64_t ldw, int64_t K, const void* s13, const uint8_t* z13, int64_t group,

@@ -103,6 +103,7 @@ int qlin_glu_w4_bwd(const void* dy, int64_t lddy, int64_t M, int64_t I, int dtyp
     if (rc != QLIN_OK) return rc;
     if (lddy < I || (gu ? ldgu < 2 * I : ldx < K) || ldw < K / 2 || ldw > kMaxPitch || lddgu < 2 * I || (dx && lddx < K))
         return QLIN_ERR_STRIDE;
+    if (gu == dgu && ldgu != lddgu && M > 1) return QLIN_ERR_STRIDE;  // a row written before another is read
     if (misaligned(dy, 2) || (gu ? misaligned(gu, 2) : misaligned(x, 16) || ldx % 8 != 0) ||
         weight_misaligned(w13, ldw, s13) || misaligned(dgu, 16) || lddgu % 8 != 0 || (dx && misaligned(dx, 2)))
         return QLIN_ERR_ALIGN;
