@@ -452,7 +452,8 @@ def _out16(t, name, like, rows, cols, stream=None):
     if t is None:
         return _own(name, (rows, cols), like.dtype, like, stream)
     if (isinstance(t, torch.Tensor) and t.dtype is like.dtype and t.dim() == 2
-            and t.shape[0] == rows and t.shape[1] == cols and (t.stride(1) == 1 or cols == 1) and t.get_device() == like.get_device()):
+            and t.shape[0] == rows and t.shape[1] == cols and (t.stride(1) == 1 or cols == 1)
+            and t.get_device() == like.get_device()):
         return t
     _need(t, name, (like.dtype,), 2)
     raise ValueError(f"{name} must be [{rows}, {cols}] on {like.device}, got {tuple(t.shape)} on {t.device}")
