@@ -7,7 +7,8 @@
  * E4M3 / E5M2 codes), 128x128 block-scaled FP8 with UE8M0 scales, the
  * MXFP4 expert GEMV behind top-k routing (also as a routed expert FFN), and
  * 4-bit weights with group scales (also as a gated feed-forward front, and
- * both with their input gradients).
+ * both with their input gradients).  On INT8 weights there are also a gated
+ * feed-forward front and a routed expert layer.
  *
  * Sources (web pages, by title and section):
  *   [Z100] "Hygon Z100 (gfx906) vLLM adaptation: optimisation and operator
@@ -445,6 +446,68 @@ int qlin_glu_w4_bwd(const void* dy, int64_t lddy, int64_t M, int64_t I, int dtyp
                     const void* x, int64_t ldx, const void* gu, int64_t ldgu,
                     const uint8_t* w13, int64_t ldw, int64_t K, const void* s13, const uint8_t* z13, int64_t group,
                     void* dgu, int64_t lddgu, void* dx, int64_t lddx,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * (g) INT8 feed-forward: gated front and routed expert layer (W8A8, a scale
+ *     per token and per output channel)
+ * ------------------------------------------------------------------------
+ * Rows are quantised by the rule of qlin_act_quant_i8, for bf16 or fp16 values:
+ *   s = max_k |v[k]| / 127,  q = clamp(rne(v / s), -127, 127)
+ * (IEEE fp32 quotients; an all-zero row has s = 0 and codes 0).  A row that
+ * holds an infinity or a NaN has s = NaN and codes 0: the outputs that it feeds
+ * are NaN, and no others.  dtype is the type of x and y.  K, H and I as
+ * reduction lengths are multiples of 16 in [16, 131072]; 1 <= M <=
+ * QLIN_MAX_M_PREFILL; row pitches at most 2^30 elements. */
+
+/* Gated front.  w13 has 2I rows: gate rows 0..I-1, then up rows I..2I-1.
+ *   xq, xs  codes [M, ldxq] and scales [M] of x (outputs, always written)
+ *   g[m,i] = (fp32(sum_k xq[m,k] w13[i,k]) * xs[m]) * s13[i],  u with row I+i
+ *   y[m,i] = r16( act(g) * u )                           16-bit [M, ldy]
+ *   x 16-bit [M, ldx]; s13 fp32 [2I] (ws_per_row = 1) or [1] (= 0)
+ * The int32 sums are exact; act is QLIN_ACT_*.  1 <= I <= 2^20.  The down
+ * projection is qlin_linear_i8 on y (bf16).  Alignment: x, w13, xq 16 bytes,
+ * ldx % 8 == 0, ldw % 16 == 0, ldxq % 16 == 0. */
+int qlin_glu_i8(const void* x, int64_t ldx, int64_t M, int64_t K, int dtype,
+                const int8_t* w13, int64_t ldw, int64_t I, const float* s13, int ws_per_row, int act,
+                int8_t* xq, int64_t ldxq, float* xs, void* y, int64_t ldy, void* stream);
+
+enum {
+    QLIN_ROUTE_SELECTED = 0, /* softmax over the selected experts' logits */
+    QLIN_ROUTE_ALL = 1       /* softmax over all experts' logits, not renormalised */
+};
+
+/* Bytes of device workspace qlin_moe_ffn_i8 needs (0 for sizes it refuses). */
+size_t qlin_moe_ffn_i8_workspace_bytes(int64_t M, int64_t H, int64_t I, int64_t topk, int64_t E);
+
+/* A whole mixture-of-experts layer from the router's logits.  Token t:
+ *   ids[t,:] = the topk largest of logits[t,:], largest first, equal logits to
+ *              the lower expert.  NaN and -inf mask an expert: it is never
+ *              selected, and a slot for which none is left has id -1, weight 0
+ *   gw[t,j]  = exp(logit_j - logit_0) / sum over the selected experts
+ *              (QLIN_ROUTE_SELECTED) or over all that are not masked (_ALL);
+ *              equal logits count as difference 0, infinite ones too
+ * or, with logits NULL, ids and gw are inputs; an id outside [0, E) then
+ * contributes nothing, and its weight is not looked at.  For every slot with expert e:
+ *   h[t,j,i] = r16( act(g) * u )  as qlin_glu_i8 of x[t] with w13[e], s13[e]
+ *   hq, hs   = its codes and scale
+ *   y[t,n]   = r16( sum_j gw[t,j] * ((fp32(sum_i hq[t,j,i] w2[e,n,i]) * hs[t,j]) * s2[e,n]) )
+ * added in slot order; a token without any has a row of zeros.  Results do
+ * not depend on timing, and a token's row not on the rest of the batch.
+ *   x 16-bit [M, ldx]; logits fp32 [M, ldl] or NULL
+ *   w13 int8 [E, 2I, ldw13] (gate rows, then up rows), s13 fp32 [E, 2I]
+ *   w2  int8 [E, H, ldw2], s2 fp32 [E, H]
+ *   ids int32 [M, topk], gw fp32 [M, topk] (outputs with logits, else inputs)
+ *   y 16-bit [M, ldy]; overlaps no input
+ *   workspace: 16-byte aligned, at least qlin_moe_ffn_i8_workspace_bytes();
+ *      its contents on entry do not matter; calls that can overlap need one each.
+ * 1 <= E <= 1024, 1 <= topk <= 16, with logits topk <= E.  Alignment: x, w13, w2
+ * 16 bytes, ldx % 8 == 0, ldw13 % 16 == 0, ldw2 % 16 == 0. */
+int qlin_moe_ffn_i8(const void* x, int64_t ldx, int64_t M, int64_t H, int dtype,
+                    const float* logits, int64_t ldl, int64_t E, int64_t topk, int route,
+                    const int8_t* w13, int64_t ldw13, const float* s13, int64_t I,
+                    const int8_t* w2, int64_t ldw2, const float* s2, int act,
+                    int32_t* ids, float* gw, void* y, int64_t ldy,
                     void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus

@@ -17,7 +17,7 @@ from __future__ import annotations
 import torch
 
 from ._lib import (QLIN_ACT_GELU_TANH, QLIN_ACT_SILU, QLIN_DT_BF16, QLIN_DT_FP16, QLIN_FMT_E4M3,  # noqa: F401
-                   QLIN_FMT_E5M2, QlinError, check, load, status_str)
+                   QLIN_FMT_E5M2, QLIN_ROUTE_ALL, QLIN_ROUTE_SELECTED, QlinError, check, load, status_str)
 
 __all__ = [
     "QlinError", "qlin_act_quant_i8", "qlin_gemv_i8", "qlin_linear_i8", "qlin_gemv_fp8", "qlin_gemv_fp8_blk",
@@ -25,6 +25,7 @@ __all__ = [
     "qlin_moe_mxfp4", "qlin_moe_mxfp4_workspace_bytes", "qlin_moe_mxfp4_noalloc", "status_str",
     "qlin_gemv_w4", "qlin_gemv_w4_bwd", "qlin_gemv_w4_bwd_workspace_bytes", "qlin_glu_w4", "qlin_glu_w4_bwd",
     "QLIN_DT_BF16", "QLIN_DT_FP16", "QLIN_ACT_SILU", "QLIN_ACT_GELU_TANH",
+    "qlin_glu_i8", "qlin_moe_ffn_i8", "qlin_moe_ffn_i8_workspace_bytes", "QLIN_ROUTE_SELECTED", "QLIN_ROUTE_ALL",
 ]
 
 
@@ -583,3 +584,106 @@ def qlin_glu_w4_bwd(dy, w13, s13, z13=None, act=QLIN_ACT_SILU, x=None, gu=None, 
             w13.data_ptr(), _wpitch(w13), K, s13.data_ptr(), _ptr(z13), group, dgu.data_ptr(), _pitch(dgu, M, N),
             _ptr(dx), 0 if dx is None else _pitch(dx, M, K), _ptr(buf), size)
     return dx, dgu
+
+
+# ----------------------------------------------------------------------------- INT8 feed-forward
+
+def _operand(t, name, dtype, shape, dev, dense=True):
+    """An operand of a type, shape and device; rows contiguous, or with dense=False of any pitch."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev
+                and (t.is_contiguous() if dense else t.stride(-1) == 1 or shape[-1] == 1)):
+            return t
+    except (AttributeError, RuntimeError):  # no tensor, or no strided one
+        pass
+    _need(t, name, (dtype,), len(shape))
+    raise ValueError(f"{name} must be {'contiguous ' if dense else ''}{tuple(shape)} on cuda:{dev}, got {tuple(t.shape)} "
+                     f"(strides {t.stride()}) on {t.device}")
+
+
+def _x16(x):
+    """The 16-bit activations of a call: (rows, row length, dtype flag, device index)."""
+    if not isinstance(x, torch.Tensor) or x.dtype not in _DT16 or x.dim() != 2 or not x.is_cuda or x.stride(1) != 1:
+        _need(x, "x", tuple(_DT16), 2)
+    return x.shape[0], x.shape[1], _DT16[x.dtype], x.get_device()
+
+
+def qlin_glu_i8(x, w13, s13, act=QLIN_ACT_SILU, xq=None, xs=None, y=None, stream=None):
+    """Gated feed-forward front on INT8 weights: x bf16 or fp16 [M, K]; w13 int8
+    [2I, K] (gate rows, then up rows; any row pitch that is a multiple of 16); s13
+    fp32 [2I] or [1].  x is quantised per token (codes and scales into xq int8 [M, K]
+    / xs fp32 [M]).  Returns (y [M, I] of x's dtype, xq, xs)."""
+    M, K, dt, dev = _x16(x)
+    _operand(w13, "w13", torch.int8, (w13.shape[0] if isinstance(w13, torch.Tensor) and w13.dim() == 2 else 0, K), dev,
+             False)
+    N = w13.shape[0]
+    if N % 2:
+        raise ValueError(f"w13 has {N} rows: 2I are needed")
+    _operand(s13, "s13", torch.float32, (1,) if isinstance(s13, torch.Tensor) and s13.numel() == 1 else (N,), dev)
+    xq = (_own(None, (M, K), torch.int8, x, stream) if xq is None
+          else _operand(xq, "xq", torch.int8, (M, K), dev, False))
+    xs = _own(None, (M,), torch.float32, x, stream) if xs is None else _operand(xs, "xs", torch.float32, (M,), dev)
+    y = _own(None, (M, N // 2), x.dtype, x, stream) if y is None else _operand(y, "y", x.dtype, (M, N // 2), dev, False)
+    _launch(load().qlin_glu_i8, "qlin_glu_i8", dev, stream, x.data_ptr(), _pitch(x, M, K), M, K, dt, w13.data_ptr(),
+            _wpitch(w13), N // 2, s13.data_ptr(), int(s13.shape[0] > 1), act, xq.data_ptr(),
+            xq.stride(0) if M > 1 else K, xs.data_ptr(), y.data_ptr(), _pitch(y, M, N // 2))
+    return y, xq, xs
+
+
+def qlin_moe_ffn_i8_workspace_bytes(M: int, H: int, I: int, topk: int, E: int) -> int:
+    return int(load().qlin_moe_ffn_i8_workspace_bytes(M, H, I, topk, E))
+
+
+def _experts(w, name, rows, cols, dev):
+    """Expert matrices int8 [E, rows, cols]: any row pitch, the experts one behind the other; returns the row pitch."""
+    _operand(w, name, torch.int8, (w.shape[0] if isinstance(w, torch.Tensor) and w.dim() == 3 else 0, rows, cols), dev,
+             False)
+    pitch = w.stride(1) if rows > 1 else (w.stride(0) if w.shape[0] > 1 else cols)
+    if w.shape[0] > 1 and w.stride(0) != rows * pitch:
+        raise ValueError(f"{name}: the experts must lie one behind the other, strides {w.stride()}")
+    return pitch
+
+
+def qlin_moe_ffn_i8(x, w13, s13, w2, s2, logits=None, topk=None, route=QLIN_ROUTE_SELECTED, act=QLIN_ACT_SILU, ids=None,
+                    gw=None, y=None, workspace=None, stream=None):
+    """Mixture-of-experts layer on INT8 experts: x bf16 or fp16 [M, H]; w13 int8
+    [E, 2I, H] (gate rows, then up rows), s13 fp32 [E, 2I]; w2 int8 [E, H, I], s2 fp32
+    [E, H].  logits fp32 [M, E]: the router's; topk experts of each token are selected
+    on the device (NaN and -inf mask an expert) and written to ids int32 [M, topk] / gw
+    fp32 [M, topk].  Without logits ids and gw are inputs; an id outside the experts
+    contributes nothing.  Returns (y [M, H] of x's dtype, ids, gw)."""
+    M, H, dt, dev = _x16(x)
+    if not isinstance(w13, torch.Tensor) or not isinstance(w2, torch.Tensor) or w13.dim() != 3 or w2.dim() != 3:
+        _need(w13, "w13", (torch.int8,), 3)
+        _need(w2, "w2", (torch.int8,), 3)
+    E, I = w13.shape[0], w2.shape[2]
+    p13, p2 = _experts(w13, "w13", 2 * I, H, dev), _experts(w2, "w2", H, I, dev)
+    if w2.shape[0] != E:
+        raise ValueError(f"w13 has {E} experts, w2 {w2.shape[0]}")
+    _operand(s13, "s13", torch.float32, (E, 2 * I), dev)
+    _operand(s2, "s2", torch.float32, (E, H), dev)
+    if logits is not None:
+        if topk is None:
+            raise ValueError("topk is needed along with logits")
+        _operand(logits, "logits", torch.float32, (M, E), dev, False)
+        ids = _own(None, (M, topk), torch.int32, x, stream) if ids is None else _operand(ids, "ids", torch.int32, (M, topk), dev)
+        gw = _own(None, (M, topk), torch.float32, x, stream) if gw is None else _operand(gw, "gw", torch.float32, (M, topk), dev)
+    else:
+        if ids is None or gw is None:
+            raise ValueError("either logits or ids and gw are needed")
+        if topk is None and isinstance(ids, torch.Tensor) and ids.dim() == 2:
+            topk = ids.shape[1]
+        _operand(ids, "ids", torch.int32, (M, topk), dev)
+        _operand(gw, "gw", torch.float32, (M, topk), dev)
+    y = _own(None, (M, H), x.dtype, x, stream) if y is None else _operand(y, "y", x.dtype, (M, H), dev, False)
+    lib = load()
+    if workspace is None:
+        need = lib.qlin_moe_ffn_i8_workspace_bytes(M, H, I, topk, E)
+        workspace = _own(None, (max(need, 1),), torch.uint8, x, stream)
+    elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {x.device}")
+    _launch(lib.qlin_moe_ffn_i8, "qlin_moe_ffn_i8", dev, stream, x.data_ptr(), _pitch(x, M, H), M, H, dt,
+            _ptr(logits), 0 if logits is None else (logits.stride(0) if M > 1 else E), E, topk, route, w13.data_ptr(), p13,
+            s13.data_ptr(), I, w2.data_ptr(), p2, s2.data_ptr(), act, ids.data_ptr(), gw.data_ptr(), y.data_ptr(),
+            _pitch(y, M, H), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return y, ids, gw

@@ -27,6 +27,7 @@ EXPORTS = (
     "qlin_moe_ffn_mxfp4_workspace_bytes", "qlin_moe_ffn_mxfp4", "qlin_act_quant_fp8", "qlin_gemv_fp8_w8a8",
     "qlin_gemv_fp8_blk_ex", "qlin_moe_mxfp4_noalloc", "qlin_linear_i8",
     "qlin_gemv_w4", "qlin_gemv_w4_bwd_workspace_bytes", "qlin_gemv_w4_bwd", "qlin_glu_w4", "qlin_glu_w4_bwd",
+    "qlin_glu_i8", "qlin_moe_ffn_i8_workspace_bytes", "qlin_moe_ffn_i8",
 )
 
 QLIN_FMT_E4M3 = 0
@@ -37,6 +38,9 @@ QLIN_DT_FP16 = 1
 
 QLIN_ACT_SILU = 0
 QLIN_ACT_GELU_TANH = 1
+
+QLIN_ROUTE_SELECTED = 0
+QLIN_ROUTE_ALL = 1
 
 
 class QlinError(RuntimeError):
@@ -99,6 +103,13 @@ def load() -> ctypes.CDLL:
     lib.qlin_glu_w4_bwd.argtypes = [P, I64, I64, I64, I, I, P, I64, P, I64, P, I64, I64, P, P, I64, P, I64, P, I64,
                                     P, SZ, P]
     lib.qlin_glu_w4_bwd.restype = I
+    lib.qlin_glu_i8.argtypes = [P, I64, I64, I64, I, P, I64, I64, P, I, I, P, I64, P, P, I64, P]
+    lib.qlin_glu_i8.restype = I
+    lib.qlin_moe_ffn_i8_workspace_bytes.argtypes = [I64, I64, I64, I64, I64]
+    lib.qlin_moe_ffn_i8_workspace_bytes.restype = SZ
+    lib.qlin_moe_ffn_i8.argtypes = [P, I64, I64, I64, I, P, I64, I64, I64, I, P, I64, P, I64, P, I64, P, I, P, P,
+                                    P, I64, P, SZ, P]
+    lib.qlin_moe_ffn_i8.restype = I
     _lib = lib
     return lib
 

@@ -1,0 +1,252 @@
+// i8ffn.hip -- the INT8 feed-forward operators: row quantiser, routing, pair
+// sort and combine kernels, and the launchers of the gated front
+// (qlin_glu_i8) and the routed expert layer (qlin_moe_ffn_i8).
+#include "i8ffn_gemm.hpp"
+#include "i8ffn_launch.hpp"
+
+namespace qlin {
+
+namespace {
+
+// One workgroup per row: largest magnitude, then codes (i8ffn_device.hpp).
+// ids, if given: a row whose id is outside [0, E) is not read or written.
+constexpr int kI8QuantThreads = 512;
+
+template <int T>
+__global__ __launch_bounds__(kI8QuantThreads) void i8_quant_kernel(const uint16_t* x, int64_t ldx, int64_t K, int8_t* xq,
+                                                                   int64_t ldxq, float* xs, const int32_t* ids, int E) {
+    constexpr int W = kI8QuantThreads / 64, CACHED = 2;
+    __shared__ uint32_t part[W];
+    const int64_t m = blockIdx.x;
+    if (ids && (uint32_t)ids[m] >= (uint32_t)E) return;  // workgroup-uniform
+    const uint16_t* row = x + m * ldx;
+    const int tid = threadIdx.x;
+    const int64_t nvec = K >> 3;
+    u32x4_t cache[CACHED];
+    uint32_t a = 0;
+#pragma unroll
+    for (int c = 0; c < CACHED; ++c) {
+        const int64_t i = tid + c * kI8QuantThreads;
+        cache[c] = i < nvec ? ld16(row + i * 8) : u32x4_t{0, 0, 0, 0};
+        a = mag8(cache[c], a);
+    }
+    for (int64_t i = tid + CACHED * kI8QuantThreads; i < nvec; i += kI8QuantThreads) a = mag8(ld16(row + i * 8), a);
+    a = wave_mag(a);
+    if ((tid & 63) == 0) part[tid >> 6] = a;
+    __syncthreads();
+    uint32_t mag = part[0];
+#pragma unroll
+    for (int q = 1; q < W; ++q) mag = part[q] > mag ? part[q] : mag;
+    double r;
+    const float s = row_scale<T>(mag, r);
+    if (tid == 0) xs[m] = s;
+    int8_t* out = xq + m * ldxq;
+#pragma unroll
+    for (int c = 0; c < CACHED; ++c) {
+        const int64_t i = tid + c * kI8QuantThreads;
+        if (i < nvec) *(uint2*)(out + i * 8) = codes8<T>(cache[c], r);
+    }
+    for (int64_t i = tid + CACHED * kI8QuantThreads; i < nvec; i += kI8QuantThreads)
+        *(uint2*)(out + i * 8) = codes8<T>(ld16(row + i * 8), r);
+}
+
+hipError_t quantise(int dtype, const uint16_t* x, int64_t ldx, int64_t rows, int64_t K, int8_t* xq, int64_t ldxq, float* xs,
+                    const int32_t* ids, int64_t E, hipStream_t st) {
+    auto k = dtype == kFp16 ? i8_quant_kernel<kFp16> : i8_quant_kernel<kBf16>;
+    hipLaunchKernelGGL(k, dim3((unsigned)rows), dim3(kI8QuantThreads), 0, st, x, ldx, K, xq, ldxq, xs, ids, (int)E);
+    return hipGetLastError();
+}
+
+// One wave per token.
+template <int NR>
+__global__ __launch_bounds__(256) void i8_route_kernel(const float* logits, int64_t ldl, int M, int E, int topk, int route,
+                                                       int32_t* ids, float* gw) {
+    const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    if (m >= M) return;
+    int id;
+    float w;
+    route_token<NR>(logits + m * ldl, E, topk, route, lane, id, w);
+    if (lane < topk) {
+        ids[m * topk + lane] = id;
+        gw[m * topk + lane] = w;
+    }
+}
+
+hipError_t route(const I8MoeArgs& a, hipStream_t st) {
+    auto k = a.E <= 64 ? i8_route_kernel<1> : (a.E <= 128 ? i8_route_kernel<2> : (a.E <= 256 ? i8_route_kernel<4> : i8_route_kernel<16>));
+    hipLaunchKernelGGL(k, dim3((unsigned)((a.M + 3) / 4)), dim3(256), 0, st, a.logits, a.ldl, (int)a.M, (int)a.E,
+                       (int)a.topk, a.route, a.ids, a.gw);
+    return hipGetLastError();
+}
+
+// Pairs by expert: offs the first of each expert's pairs in perm, toffs the
+// first of its tiles of bm pairs.  One workgroup, LDS counters: the order of an
+// expert's pairs is arbitrary, which no result depends on (every pair's row is
+// computed on its own, the combine adds in slot order).
+constexpr int kI8MaxE = 1024;
+
+__global__ __launch_bounds__(1024) void i8_sort_kernel(const int32_t* ids, int P, int E, int bm, int32_t* offs,
+                                                       int32_t* toffs, int32_t* perm) {
+    __shared__ int32_t cnt[kI8MaxE], cur[kI8MaxE], wsum[16], wtile[16];
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+    cnt[tid] = 0;
+    __syncthreads();
+    for (int p = tid; p < P; p += 1024) {
+        const int32_t e = ids[p];
+        if ((uint32_t)e < (uint32_t)E) atomicAdd(&cnt[e], 1);
+    }
+    __syncthreads();
+    const int c = cnt[tid], t = (c + bm - 1) / bm;
+    int ci = c, ti = t;  // inclusive sums
+#pragma unroll
+    for (int s = 1; s < 64; s *= 2) {
+        const int a = __shfl_up(ci, s), b = __shfl_up(ti, s);
+        if (lane >= s) {
+            ci += a;
+            ti += b;
+        }
+    }
+    if (lane == 63) {
+        wsum[wv] = ci;
+        wtile[wv] = ti;
+    }
+    __syncthreads();
+    for (int q = 0; q < wv; ++q) {
+        ci += wsum[q];
+        ti += wtile[q];
+    }
+    cur[tid] = ci - c;
+    if (tid <= E) {  // experts past E count nothing: entry E is the total
+        offs[tid] = ci - c;
+        toffs[tid] = ti - t;
+    }
+    if (tid == kI8MaxE - 1 && E == kI8MaxE) {
+        offs[E] = ci;
+        toffs[E] = ti;
+    }
+    __syncthreads();
+    for (int p = tid; p < P; p += 1024) {
+        const int32_t e = ids[p];
+        if ((uint32_t)e < (uint32_t)E) perm[atomicAdd(&cur[e], 1)] = p;
+    }
+}
+
+// y[t,n] = r16(sum_j gw[t,j] part[t,j,n]) in slot order, four columns a thread.
+template <int T>
+__global__ __launch_bounds__(256) void i8_combine_kernel(const float* part, const int32_t* ids, const float* gw, int64_t M,
+                                                         int topk, int E, int64_t N, uint16_t* y, int64_t ldy) {
+    const int64_t nv = N / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // N % 16 == 0
+    if (i >= M * nv) return;
+    const int64_t t = i / nv, n = (i - t * nv) * 4;
+    f32x4v_t sum = {0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < topk; ++j) {
+        const int64_t p = t * topk + j;
+        if ((uint32_t)ids[p] >= (uint32_t)E) continue;
+        const f32x4v_t v = __builtin_nontemporal_load((const f32x4v_t*)(part + p * N + n));
+        const float g = gw[p];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sum[c] = fmaf(g, v[c], sum[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) y[t * ldy + n + c] = f32_to_h<T>(sum[c]);
+}
+
+template <int T, int EPI, int BN, int BM, int WGN, int WGM>
+hipError_t run_gemm(const I8GemmParams& p, int64_t row_tiles, hipStream_t st) {
+    constexpr int CT = EPI == kI8Gated ? BN / 2 : BN;
+    const int64_t tiles = row_tiles * ((p.C + CT - 1) / CT);
+    hipLaunchKernelGGL((i8_gemm_kernel<T, EPI, BN, BM, WGN, WGM>), dim3((unsigned)((tiles + 7) / 8 * 8)),
+                       dim3(64 * WGN * WGM), 0, st, p);
+    return hipGetLastError();
+}
+
+// row tiles that P pairs of E groups can make at most
+int64_t most_tiles(int64_t P, int64_t E, int64_t bm) { return P / bm + (E < P ? E : P); }
+
+constexpr int kI8Bm = 64;
+
+struct MoeRegions { size_t xq, xs, h, hq, hs, part, offs, toffs, perm, total; };
+
+MoeRegions regions(int64_t M, int64_t H, int64_t I, int64_t topk, int64_t E) {
+    MoeRegions r{};
+    size_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const size_t here = at;
+        at += ((size_t)bytes + 255) / 256 * 256;
+        return here;
+    };
+    const int64_t P = M * topk;
+    r.xq = take(M * H);
+    r.xs = take(M * 4);
+    r.h = take(P * I * 2);
+    r.hq = take(P * I);
+    r.hs = take(P * 4);
+    r.part = take(P * H * 4);
+    r.offs = take((E + 1) * 4);
+    r.toffs = take((E + 1) * 4);
+    r.perm = take(P * 4);
+    r.total = at;
+    return r;
+}
+
+template <int T>
+hipError_t moe(const I8MoeArgs& a, hipStream_t st) {
+    const MoeRegions r = regions(a.M, a.H, a.I, a.topk, a.E);
+    const int64_t P = a.M * a.topk;
+    uint8_t* ws = a.workspace;
+    int8_t *xq = (int8_t*)(ws + r.xq), *hq = (int8_t*)(ws + r.hq);
+    float *xs = (float*)(ws + r.xs), *hs = (float*)(ws + r.hs), *part = (float*)(ws + r.part);
+    uint16_t* h = (uint16_t*)(ws + r.h);
+    int32_t *offs = (int32_t*)(ws + r.offs), *toffs = (int32_t*)(ws + r.toffs), *perm = (int32_t*)(ws + r.perm);
+    hipError_t e = a.logits ? route(a, st) : hipSuccess;
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(i8_sort_kernel, dim3(1), dim3(1024), 0, st, a.ids, (int)P, (int)a.E, kI8Bm, offs, toffs, perm);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    e = quantise(T, a.x, a.ldx, a.M, a.H, xq, a.H, xs, nullptr, 0, st);
+    if (e != hipSuccess) return e;
+    I8GemmParams g{};
+    g.x = xq; g.ldx = a.H; g.xs = xs; g.offs = offs; g.toffs = toffs; g.perm = perm; g.div = (int)a.topk; g.E = (int)a.E;
+    g.K = a.H; g.w = a.w13; g.ldw = a.ldw13; g.N = 2 * a.I; g.ws = a.s13; g.ws_step = 1; g.C = a.I; g.act = a.act;
+    g.y = h; g.ldy = a.I;
+    e = run_gemm<T, kI8Gated, 128, kI8Bm, 2, 2>(g, most_tiles(P, a.E, kI8Bm), st);
+    if (e != hipSuccess) return e;
+    e = quantise(T, h, a.I, P, a.I, hq, a.I, hs, a.ids, a.E, st);
+    if (e != hipSuccess) return e;
+    g.x = hq; g.ldx = a.I; g.xs = hs; g.div = 1; g.K = a.I; g.w = a.w2; g.ldw = a.ldw2; g.N = a.H; g.ws = a.s2;
+    g.C = a.H; g.y = nullptr; g.part = part; g.ldy = a.H;
+    e = run_gemm<T, kI8Part, 128, kI8Bm, 2, 2>(g, most_tiles(P, a.E, kI8Bm), st);
+    if (e != hipSuccess) return e;
+    const int64_t n = a.M * (a.H / 4);
+    hipLaunchKernelGGL(i8_combine_kernel<T>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, part, a.ids, a.gw, a.M,
+                       (int)a.topk, (int)a.E, a.H, a.y, a.ldy);
+    return hipGetLastError();
+}
+
+template <int T>
+hipError_t glu(const I8GluArgs& a, hipStream_t st) {
+    const hipError_t e = quantise(T, a.x, a.ldx, a.M, a.K, a.xq, a.ldxq, a.xs, nullptr, 0, st);
+    if (e != hipSuccess) return e;
+    I8GemmParams g{};
+    g.x = a.xq; g.ldx = a.ldxq; g.xs = a.xs; g.R = a.M; g.E = 1; g.div = 1;
+    g.K = a.K; g.w = a.w13; g.ldw = a.ldw; g.N = 2 * a.I; g.ws = a.s13; g.ws_step = a.ws_step; g.C = a.I; g.act = a.act;
+    g.y = a.y; g.ldy = a.ldy;
+    return run_gemm<T, kI8Gated, 128, 64, 2, 2>(g, (a.M + 63) / 64, st);
+}
+
+}  // namespace
+
+size_t moe_ffn_i8_workspace_bytes(int64_t M, int64_t H, int64_t I, int64_t topk, int64_t E) {
+    return regions(M, H, I, topk, E).total;
+}
+
+hipError_t launch_glu_i8(const I8GluArgs& a, hipStream_t st) {
+    return a.dtype == kFp16 ? glu<kFp16>(a, st) : glu<kBf16>(a, st);
+}
+
+hipError_t launch_moe_ffn_i8(const I8MoeArgs& a, hipStream_t st) {
+    return a.dtype == kFp16 ? moe<kFp16>(a, st) : moe<kBf16>(a, st);
+}
+
+}  // namespace qlin

@@ -1,0 +1,150 @@
+// i8ffn_device.hpp -- quantisation rule, routing and epilogue arithmetic shared
+// by the INT8 feed-forward kernels.
+//
+// Quantisation of a row (the INT8 rule of qlin_device.hpp, for either 16-bit
+// type): s = amax / 127 and q = clamp(rne(x / s)), both quotients IEEE fp32;
+// amax = 0 gives s = 0 and codes 0.  The maximum is taken over the magnitude
+// bits as whole numbers, which order like the values and put infinities and
+// NaNs above every finite one: a row that holds one gets s = NaN and codes 0,
+// so all it feeds is NaN and no other row is touched.
+#pragma once
+#include "w4_device.hpp"
+
+namespace qlin {
+
+// largest 16-bit magnitude (sign cleared) of 8 values, as a whole number; two halves in one register
+__device__ __forceinline__ uint32_t pk_max_u16(uint32_t a, uint32_t b) {
+    typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+    const u16x2_t r = __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a), __builtin_bit_cast(u16x2_t, b));
+    return __builtin_bit_cast(uint32_t, r);
+}
+
+__device__ __forceinline__ uint32_t mag8(const u32x4_t& v, uint32_t m) {
+    m = pk_max_u16(m, v.x & 0x7FFF7FFFu);
+    m = pk_max_u16(m, v.y & 0x7FFF7FFFu);
+    m = pk_max_u16(m, v.z & 0x7FFF7FFFu);
+    return pk_max_u16(m, v.w & 0x7FFF7FFFu);
+}
+
+// the larger half of the packed maximum, over the whole wave
+__device__ __forceinline__ uint32_t wave_mag(uint32_t m) {
+    m = pk_max_u16(m, (uint32_t)dpp_mov<0x128>((int)m));
+    m = pk_max_u16(m, (uint32_t)dpp_mov<0x124>((int)m));
+    m = pk_max_u16(m, (uint32_t)dpp_mov<0x122>((int)m));
+    m = pk_max_u16(m, (uint32_t)dpp_mov<0x121>((int)m));
+    m = pk_max_u16(m, (uint32_t)__shfl_xor((int)m, 16));
+    m = pk_max_u16(m, (uint32_t)__shfl_xor((int)m, 32));
+    const uint32_t lo = m & 0xFFFFu, hi = m >> 16;
+    return lo > hi ? lo : hi;
+}
+
+// s and fl64(1 / s) (0 where the codes are 0) of a row whose largest magnitude has the bits `mag`
+template <int T>
+__device__ __forceinline__ float row_scale(uint32_t mag, double& r) {
+    const uint32_t inf = T == kBf16 ? 0x7F80u : 0x7C00u;
+    const float s = mag >= inf ? __uint_as_float(0x7FC00000u) : h_to_f32<T>(mag) / 127.0f;
+    r = mag == 0 || mag >= inf ? 0.0 : 1.0 / (double)s;
+    return s;
+}
+
+// 8 values -> 8 codes; r = 0 gives codes 0 (a non-finite value times 0 is NaN, which v_cvt_i32_f32 turns into 0)
+template <int T>
+__device__ __forceinline__ uint2 codes8(const u32x4_t& v, double r) {
+    const uint32_t d[4] = {v.x, v.y, v.z, v.w};
+    uint32_t packed[2] = {0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t h = (e & 1) ? (d[e >> 1] >> 16) : (d[e >> 1] & 0xFFFFu);
+        float t = rintf(div_bf16(h_to_f32<T>(h), r));
+        t = fminf(fmaxf(t, -127.0f), 127.0f);
+        packed[e >> 2] |= ((uint32_t)(r == 0.0 ? 0 : (int)t) & 0xFFu) << (8 * (e & 3));
+    }
+    return make_uint2(packed[0], packed[1]);
+}
+
+// act(g) u of the int32 sums of a gate and an up row
+__device__ __forceinline__ float gated(int ag, int au, float xs, float sg, float su, int act) {
+    float a, da;
+    gate_act(((float)ag * xs) * sg, act, a, da);
+    return a * (((float)au * xs) * su);
+}
+
+// ---------------------------------------------------------------- routing
+constexpr int kRouteSelected = 0;  // values of the C ABI's route argument
+constexpr int kRouteAll = 1;
+
+// A logit as a whole number of the same order; 0 where the expert is masked (NaN or -inf).  -0 counts as 0.
+__device__ __forceinline__ uint32_t route_key(float l) {
+    const uint32_t u = __float_as_uint(l + 0.0f);
+    return l > -INFINITY ? ((u >> 31) ? ~u : u | 0x80000000u) : 0u;
+}
+__device__ __forceinline__ float route_logit(uint32_t key) {
+    return __uint_as_float((key >> 31) ? key & 0x7FFFFFFFu : ~key);
+}
+__device__ __forceinline__ float route_exp(float l, float top) { return l == top ? 1.0f : expf(l - top); }
+
+__device__ __forceinline__ float wave_sum_f32(float v) {
+    v = row_sum_f32(v);
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
+    return v;
+}
+
+// One wave routes one token: its topk largest logits, largest first, equal ones
+// to the lower expert.  Lane j < topk returns slot j's expert (-1: every
+// expert left is masked) and weight exp(l_j - l_0) / sum, over the selected
+// experts or over all.  NR x 64 >= E.
+template <int NR>
+__device__ __forceinline__ void route_token(const float* row, int E, int topk, int route, int lane, int& id, float& w) {
+    uint32_t key[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) key[i] = i * 64 + lane < E ? route_key(row[i * 64 + lane]) : 0u;
+    uint32_t all[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) all[i] = key[i];
+    id = -1;
+    uint32_t mine = 0;
+    for (int j = 0; j < topk; ++j) {
+        uint32_t best = 0;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = i;
+            }
+        uint32_t top = best;
+#pragma unroll
+        for (int s = 1; s < 64; s *= 2) {
+            const uint32_t o = (uint32_t)__shfl_xor((int)top, s);
+            top = o > top ? o : top;
+        }
+        if (top == 0) break;  // uniform
+        int e = best == top ? at * 64 + lane : 0x7FFFFFFF;
+#pragma unroll
+        for (int s = 1; s < 64; s *= 2) {
+            const int o = __shfl_xor(e, s);
+            e = o < e ? o : e;
+        }
+        if (lane == j) {
+            id = e;
+            mine = top;
+        }
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+            if (e == i * 64 + lane) key[i] = 0;
+    }
+    const uint32_t first = (uint32_t)__builtin_amdgcn_readfirstlane((int)mine);
+    const float top = route_logit(first);
+    const float x = mine ? route_exp(route_logit(mine), top) : 0.0f;
+    float part = x;
+    if (route == kRouteAll) {
+        part = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NR; ++i) part += all[i] ? route_exp(route_logit(all[i]), top) : 0.0f;
+    }
+    const float sum = wave_sum_f32(part);
+    w = mine ? x / sum : 0.0f;
+}
+
+}  // namespace qlin
