@@ -1,6 +1,9 @@
 // i8ffn.hip -- the INT8 feed-forward operators: row quantiser, routing, pair
 // sort and combine kernels, and the launchers of the gated front
 // (qlin_glu_i8) and the routed expert layer (qlin_moe_ffn_i8).
+#include <algorithm>
+
+#include "i8ffn_few.hpp"
 #include "i8ffn_gemm.hpp"
 #include "i8ffn_launch.hpp"
 
@@ -190,6 +193,70 @@ MoeRegions regions(int64_t M, int64_t H, int64_t I, int64_t topk, int64_t E) {
     return r;
 }
 
+// ---- up to 16 tokens
+constexpr int kFewLds = 150 * 1024;     // dynamic LDS next to the lists
+constexpr int kFewSums = 16 * 1024;     // of which sums
+constexpr int kFewShared = 70 * 1024;   // with which two workgroups share a compute unit
+
+bool few_fits(int64_t M, int64_t K) { return M <= kFewTokens && M * few_pitch((int)K) <= kFewLds; }
+
+// Each workgroup quantises the rows for itself, or copies the codes that a kernel ahead wrote.
+bool few_quantise(int64_t rows, int64_t K) { return rows * ((K + 511) / 512) <= kFewUnits; }
+
+template <int T, int SRC>
+hipError_t run_front(const FewFrontParams& p, hipStream_t st) {
+    const size_t lds = (size_t)p.M * few_pitch(p.K);
+    const int64_t chunks = p.E > 0 ? std::min<int64_t>(p.E, p.M * p.topk) : 1, n = chunks * ((p.I + 1) / 2);
+    const unsigned grid = (unsigned)std::min<int64_t>((n + kFewWaves - 1) / kFewWaves, lds > kFewShared ? 256 : 512);
+    auto k = p.E <= 128 ? few_front_kernel<T, SRC, 2> : few_front_kernel<T, SRC, 16>;
+    hipLaunchKernelGGL(k, dim3(grid), dim3(kFewThreads), lds, st, p);
+    return hipGetLastError();
+}
+
+template <int T>
+hipError_t few_front(FewFrontParams& p, int8_t* xq, int64_t ldxq, float* xs, hipStream_t st) {
+    p.ldxq = ldxq;
+    if (few_quantise(p.M, p.K)) {
+        p.xq_out = p.E > 0 ? nullptr : xq;
+        p.xs_out = xs;
+        return run_front<T, kFewQuantise>(p, st);
+    }
+    const hipError_t e = quantise(T, p.x, p.ldx, p.M, p.K, xq, ldxq, xs, nullptr, 0, st);
+    if (e != hipSuccess) return e;
+    p.xq = xq;
+    p.xs = xs;
+    return run_front<T, kFewStaged>(p, st);
+}
+
+template <int T, int SRC>
+hipError_t run_down(FewDownParams& p, hipStream_t st) {
+    const int P = p.M * p.topk, groups = (int)(p.H / 4), pitch = few_pitch(p.I);
+    p.rows = std::min(P, (kFewLds - kFewSums) / pitch);
+    const int grid = std::min(groups, p.rows * pitch + kFewSums > kFewShared ? 256 : 512), most = (groups + grid - 1) / grid;
+    p.block = std::max(1, std::min(most, kFewSums / (16 * P)));
+    hipLaunchKernelGGL((few_down_kernel<T, SRC>), dim3((unsigned)grid), dim3(kFewThreads),
+                       (size_t)p.block * P * 16 + (size_t)p.rows * pitch, st, p);
+    return hipGetLastError();
+}
+
+template <int T>
+hipError_t few_moe(const I8MoeArgs& a, uint16_t* h, int8_t* xq, float* xs, int8_t* hq, float* hs, hipStream_t st) {
+    const int64_t P = a.M * a.topk;
+    FewFrontParams f{};
+    f.x = a.x; f.ldx = a.ldx; f.M = (int)a.M; f.K = (int)a.H; f.logits = a.logits; f.ldl = a.ldl; f.E = (int)a.E;
+    f.topk = (int)a.topk; f.route = a.route; f.ids = a.ids; f.gw = a.gw; f.w = a.w13; f.ldw = a.ldw13; f.I = a.I;
+    f.ws = a.s13; f.ws_step = 1; f.act = a.act; f.y = h; f.ldy = a.I;
+    hipError_t e = few_front<T>(f, xq, a.H, xs, st);
+    if (e != hipSuccess) return e;
+    FewDownParams d{};
+    d.h = h; d.hq = hq; d.hs = hs; d.M = (int)a.M; d.I = (int)a.I; d.ids = a.ids; d.gw = a.gw; d.E = (int)a.E;
+    d.topk = (int)a.topk; d.w = a.w2; d.ldw = a.ldw2; d.H = a.H; d.ws = a.s2; d.y = a.y; d.ldy = a.ldy;
+    if (few_quantise(P, a.I)) return run_down<T, kFewQuantise>(d, st);
+    e = quantise(T, h, a.I, P, a.I, hq, a.I, hs, a.ids, a.E, st);
+    if (e != hipSuccess) return e;
+    return run_down<T, kFewStaged>(d, st);
+}
+
 template <int T>
 hipError_t moe(const I8MoeArgs& a, hipStream_t st) {
     const MoeRegions r = regions(a.M, a.H, a.I, a.topk, a.E);
@@ -199,6 +266,7 @@ hipError_t moe(const I8MoeArgs& a, hipStream_t st) {
     float *xs = (float*)(ws + r.xs), *hs = (float*)(ws + r.hs), *part = (float*)(ws + r.part);
     uint16_t* h = (uint16_t*)(ws + r.h);
     int32_t *offs = (int32_t*)(ws + r.offs), *toffs = (int32_t*)(ws + r.toffs), *perm = (int32_t*)(ws + r.perm);
+    if (few_fits(a.M, a.H)) return few_moe<T>(a, h, xq, xs, hq, hs, st);
     hipError_t e = a.logits ? route(a, st) : hipSuccess;
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(i8_sort_kernel, dim3(1), dim3(1024), 0, st, a.ids, (int)P, (int)a.E, kI8Bm, offs, toffs, perm);
@@ -226,6 +294,12 @@ hipError_t moe(const I8MoeArgs& a, hipStream_t st) {
 
 template <int T>
 hipError_t glu(const I8GluArgs& a, hipStream_t st) {
+    if (few_fits(a.M, a.K)) {
+        FewFrontParams f{};
+        f.x = a.x; f.ldx = a.ldx; f.M = (int)a.M; f.K = (int)a.K; f.w = a.w13; f.ldw = a.ldw; f.I = a.I; f.ws = a.s13;
+        f.ws_step = a.ws_step; f.act = a.act; f.y = a.y; f.ldy = a.ldy;
+        return few_front<T>(f, a.xq, a.ldxq, a.xs, st);
+    }
     const hipError_t e = quantise(T, a.x, a.ldx, a.M, a.K, a.xq, a.ldxq, a.xs, nullptr, 0, st);
     if (e != hipSuccess) return e;
     I8GemmParams g{};

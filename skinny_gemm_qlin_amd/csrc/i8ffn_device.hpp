@@ -32,9 +32,12 @@ __device__ __forceinline__ uint32_t wave_mag(uint32_t m) {
     m = pk_max_u16(m, (uint32_t)dpp_mov<0x124>((int)m));
     m = pk_max_u16(m, (uint32_t)dpp_mov<0x122>((int)m));
     m = pk_max_u16(m, (uint32_t)dpp_mov<0x121>((int)m));
-    m = pk_max_u16(m, (uint32_t)__shfl_xor((int)m, 16));
-    m = pk_max_u16(m, (uint32_t)__shfl_xor((int)m, 32));
-    const uint32_t lo = m & 0xFFFFu, hi = m >> 16;
+    uint32_t a = m, b = m;
+    swap32(a, b);
+    a = b = pk_max_u16(a, b);
+    swap16(a, b);
+    a = pk_max_u16(a, b);
+    const uint32_t lo = a & 0xFFFFu, hi = a >> 16;
     return lo > hi ? lo : hi;
 }
 
@@ -84,10 +87,26 @@ __device__ __forceinline__ float route_logit(uint32_t key) {
 __device__ __forceinline__ float route_exp(float l, float top) { return l == top ? 1.0f : expf(l - top); }
 
 __device__ __forceinline__ float wave_sum_f32(float v) {
-    v = row_sum_f32(v);
-    v += __shfl_xor(v, 16);
-    v += __shfl_xor(v, 32);
-    return v;
+    const uint32_t r = __float_as_uint(row_sum_f32(v));
+    uint32_t a = r, b = r;
+    swap32(a, b);
+    a = b = __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    swap16(a, b);
+    return __uint_as_float(a) + __uint_as_float(b);
+}
+
+__device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {  // uniform
+    v = max_u32(v, (uint32_t)dpp_mov<0x128>((int)v));
+    v = max_u32(v, (uint32_t)dpp_mov<0x124>((int)v));
+    v = max_u32(v, (uint32_t)dpp_mov<0x122>((int)v));
+    v = max_u32(v, (uint32_t)dpp_mov<0x121>((int)v));
+    uint32_t a = v, b = v;
+    swap32(a, b);
+    a = b = max_u32(a, b);
+    swap16(a, b);
+    return (uint32_t)__builtin_amdgcn_readfirstlane((int)max_u32(a, b));
 }
 
 // One wave routes one token: its topk largest logits, largest first, equal ones
@@ -105,26 +124,16 @@ __device__ __forceinline__ void route_token(const float* row, int E, int topk, i
     id = -1;
     uint32_t mine = 0;
     for (int j = 0; j < topk; ++j) {
-        uint32_t best = 0;
-        int at = 0;
+        uint32_t best = key[0];
 #pragma unroll
-        for (int i = 0; i < NR; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                at = i;
-            }
-        uint32_t top = best;
-#pragma unroll
-        for (int s = 1; s < 64; s *= 2) {
-            const uint32_t o = (uint32_t)__shfl_xor((int)top, s);
-            top = o > top ? o : top;
-        }
+        for (int i = 1; i < NR; ++i) best = key[i] > best ? key[i] : best;
+        const uint32_t top = wave_max_u32(best);
         if (top == 0) break;  // uniform
-        int e = best == top ? at * 64 + lane : 0x7FFFFFFF;
+        int e = -1;  // the first of the equal ones
 #pragma unroll
-        for (int s = 1; s < 64; s *= 2) {
-            const int o = __shfl_xor(e, s);
-            e = o < e ? o : e;
+        for (int i = NR - 1; i >= 0; --i) {
+            const uint64_t at = __ballot(key[i] == top);
+            if (at) e = i * 64 + __builtin_ctzll(at);
         }
         if (lane == j) {
             id = e;
