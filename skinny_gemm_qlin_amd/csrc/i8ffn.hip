@@ -18,39 +18,9 @@ constexpr int kI8QuantThreads = 512;
 template <int T>
 __global__ __launch_bounds__(kI8QuantThreads) void i8_quant_kernel(const uint16_t* x, int64_t ldx, int64_t K, int8_t* xq,
                                                                    int64_t ldxq, float* xs, const int32_t* ids, int E) {
-    constexpr int W = kI8QuantThreads / 64, CACHED = 2;
-    __shared__ uint32_t part[W];
     const int64_t m = blockIdx.x;
     if (ids && (uint32_t)ids[m] >= (uint32_t)E) return;  // workgroup-uniform
-    const uint16_t* row = x + m * ldx;
-    const int tid = threadIdx.x;
-    const int64_t nvec = K >> 3;
-    u32x4_t cache[CACHED];
-    uint32_t a = 0;
-#pragma unroll
-    for (int c = 0; c < CACHED; ++c) {
-        const int64_t i = tid + c * kI8QuantThreads;
-        cache[c] = i < nvec ? ld16(row + i * 8) : u32x4_t{0, 0, 0, 0};
-        a = mag8(cache[c], a);
-    }
-    for (int64_t i = tid + CACHED * kI8QuantThreads; i < nvec; i += kI8QuantThreads) a = mag8(ld16(row + i * 8), a);
-    a = wave_mag(a);
-    if ((tid & 63) == 0) part[tid >> 6] = a;
-    __syncthreads();
-    uint32_t mag = part[0];
-#pragma unroll
-    for (int q = 1; q < W; ++q) mag = part[q] > mag ? part[q] : mag;
-    double r;
-    const float s = row_scale<T>(mag, r);
-    if (tid == 0) xs[m] = s;
-    int8_t* out = xq + m * ldxq;
-#pragma unroll
-    for (int c = 0; c < CACHED; ++c) {
-        const int64_t i = tid + c * kI8QuantThreads;
-        if (i < nvec) *(uint2*)(out + i * 8) = codes8<T>(cache[c], r);
-    }
-    for (int64_t i = tid + CACHED * kI8QuantThreads; i < nvec; i += kI8QuantThreads)
-        *(uint2*)(out + i * 8) = codes8<T>(ld16(row + i * 8), r);
+    quantise_row_wg<T, kI8QuantThreads>(x + m * ldx, K, xq + m * ldxq, xs + m);
 }
 
 hipError_t quantise(int dtype, const uint16_t* x, int64_t ldx, int64_t rows, int64_t K, int8_t* xq, int64_t ldxq, float* xs,
@@ -169,7 +139,7 @@ int64_t most_tiles(int64_t P, int64_t E, int64_t bm) { return P / bm + (E < P ? 
 
 constexpr int kI8Bm = 64;
 
-struct MoeRegions { size_t xq, xs, h, hq, hs, part, offs, toffs, perm, total; };
+struct MoeRegions { size_t xq, xs, h, hq, hs, part, offs, toffs, perm, list, total; };
 
 MoeRegions regions(int64_t M, int64_t H, int64_t I, int64_t topk, int64_t E) {
     MoeRegions r{};
@@ -189,72 +159,114 @@ MoeRegions regions(int64_t M, int64_t H, int64_t I, int64_t topk, int64_t E) {
     r.offs = take((E + 1) * 4);
     r.toffs = take((E + 1) * 4);
     r.perm = take(P * 4);
+    r.list = take(sizeof(FewList));
     r.total = at;
     return r;
 }
 
 // ---- up to 16 tokens
-constexpr int kFewLds = 150 * 1024;     // dynamic LDS next to the lists
+constexpr int kFewLds = 146 * 1024;     // dynamic LDS next to the lists, of 160 KB
 constexpr int kFewSums = 16 * 1024;     // of which sums
-constexpr int kFewShared = 70 * 1024;   // with which two workgroups share a compute unit
+static_assert(few_pitch(131072) <= kFewLds - kFewSums, "LDS holds the longest row");
+constexpr int kFewUnitsOfGpu = 256;     // compute units: a workgroup on each
 
 bool few_fits(int64_t M, int64_t K) { return M <= kFewTokens && M * few_pitch((int)K) <= kFewLds; }
 
 // Each workgroup quantises the rows for itself, or copies the codes that a kernel ahead wrote.
 bool few_quantise(int64_t rows, int64_t K) { return rows * ((K + 511) / 512) <= kFewUnits; }
 
-template <int T, int SRC>
+// Column sets (of 4 tokens) a chunk has: all tokens where they are few, else a multiple of what an expert has on
+// average, as four sets take four times the products and code reads of one (an expert that has more is taken in two
+// chunks).
+int few_sets(int64_t M, int64_t topk, int64_t E) {
+    const int64_t most = E > 0 ? std::min(M, 4 * M * topk / E + 3) : M;
+    return most <= 4 ? 1 : (most <= 8 ? 2 : 4);
+}
+
+template <int T, int SRC, int NS>
 hipError_t run_front(const FewFrontParams& p, hipStream_t st) {
     const size_t lds = (size_t)p.M * few_pitch(p.K);
     const int64_t chunks = p.E > 0 ? std::min<int64_t>(p.E, p.M * p.topk) : 1, n = chunks * ((p.I + 1) / 2);
-    const unsigned grid = (unsigned)std::min<int64_t>((n + kFewWaves - 1) / kFewWaves, lds > kFewShared ? 256 : 512);
-    auto k = p.E <= 128 ? few_front_kernel<T, SRC, 2> : few_front_kernel<T, SRC, 16>;
+    const unsigned grid = (unsigned)std::min<int64_t>(n, kFewUnitsOfGpu);
+    auto k = SRC == kFewStaged || p.E <= 128 ? few_front_kernel<T, SRC, NS, 2>
+                                             : few_front_kernel<T, SRC, NS, SRC == kFewStaged ? 2 : 16>;
     hipLaunchKernelGGL(k, dim3(grid), dim3(kFewThreads), lds, st, p);
     return hipGetLastError();
 }
 
+template <int T, int SRC>
+hipError_t run_front(const FewFrontParams& p, int sets, hipStream_t st) {
+    if (sets == 1) return run_front<T, SRC, 1>(p, st);
+    return sets == 2 ? run_front<T, SRC, 2>(p, st) : run_front<T, SRC, 4>(p, st);
+}
+
 template <int T>
-hipError_t few_front(FewFrontParams& p, int8_t* xq, int64_t ldxq, float* xs, hipStream_t st) {
+hipError_t run_prep(const FewPrepParams& p, hipStream_t st) {
+    auto k = p.E <= 128 ? few_prep_kernel<T, 2> : few_prep_kernel<T, 16>;
+    hipLaunchKernelGGL(k, dim3((unsigned)(p.rows + (p.list ? 1 : 0))), dim3(kFewThreads), 0, st, p);
+    return hipGetLastError();
+}
+
+template <int T>
+hipError_t few_front(FewFrontParams& p, int8_t* xq, int64_t ldxq, float* xs, int sets, int cap, FewList* list,
+                     hipStream_t st) {
     p.ldxq = ldxq;
     if (few_quantise(p.M, p.K)) {
         p.xq_out = p.E > 0 ? nullptr : xq;
         p.xs_out = xs;
-        return run_front<T, kFewQuantise>(p, st);
+        return run_front<T, kFewQuantise>(p, sets, st);
     }
-    const hipError_t e = quantise(T, p.x, p.ldx, p.M, p.K, xq, ldxq, xs, nullptr, 0, st);
+    FewPrepParams q{};
+    q.x = p.x; q.ldx = p.ldx; q.rows = p.M; q.K = p.K; q.xq = xq; q.ldxq = ldxq; q.xs = xs; q.logits = p.logits;
+    q.ldl = p.ldl; q.M = p.M; q.E = p.E; q.topk = p.topk; q.route = p.route; q.cap = cap; q.ids = p.ids; q.gw = p.gw;
+    q.list = list;
+    const hipError_t e = run_prep<T>(q, st);
     if (e != hipSuccess) return e;
     p.xq = xq;
     p.xs = xs;
-    return run_front<T, kFewStaged>(p, st);
+    p.list = list;
+    return run_front<T, kFewStaged>(p, sets, st);
 }
 
+int few_down_rows(int P, int I) { return std::min(P, (kFewLds - kFewSums) / few_pitch(I)); }
+
 template <int T, int SRC>
-hipError_t run_down(FewDownParams& p, hipStream_t st) {
+hipError_t run_down(FewDownParams& p, int sets, hipStream_t st) {
     const int P = p.M * p.topk, groups = (int)(p.H / 4), pitch = few_pitch(p.I);
-    p.rows = std::min(P, (kFewLds - kFewSums) / pitch);
-    const int grid = std::min(groups, p.rows * pitch + kFewSums > kFewShared ? 256 : 512), most = (groups + grid - 1) / grid;
+    p.rows = few_down_rows(P, p.I);
+    const int grid = std::min(groups, kFewUnitsOfGpu), most = (groups + grid - 1) / grid;
     p.block = std::max(1, std::min(most, kFewSums / (16 * P)));
-    hipLaunchKernelGGL((few_down_kernel<T, SRC>), dim3((unsigned)grid), dim3(kFewThreads),
+    auto k = sets == 1 ? few_down_kernel<T, SRC, 1> : (sets == 2 ? few_down_kernel<T, SRC, 2> : few_down_kernel<T, SRC, 4>);
+    hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(kFewThreads),
                        (size_t)p.block * P * 16 + (size_t)p.rows * pitch, st, p);
     return hipGetLastError();
 }
 
 template <int T>
-hipError_t few_moe(const I8MoeArgs& a, uint16_t* h, int8_t* xq, float* xs, int8_t* hq, float* hs, hipStream_t st) {
+hipError_t few_moe(const I8MoeArgs& a, uint16_t* h, int8_t* xq, float* xs, int8_t* hq, float* hs, FewList* list,
+                   hipStream_t st) {
     const int64_t P = a.M * a.topk;
     FewFrontParams f{};
     f.x = a.x; f.ldx = a.ldx; f.M = (int)a.M; f.K = (int)a.H; f.logits = a.logits; f.ldl = a.ldl; f.E = (int)a.E;
     f.topk = (int)a.topk; f.route = a.route; f.ids = a.ids; f.gw = a.gw; f.w = a.w13; f.ldw = a.ldw13; f.I = a.I;
     f.ws = a.s13; f.ws_step = 1; f.act = a.act; f.y = h; f.ldy = a.I;
-    hipError_t e = few_front<T>(f, xq, a.H, xs, st);
+    const int sets = few_sets(a.M, a.topk, a.E), cap = std::min(4 * sets, few_down_rows((int)P, (int)a.I));
+    hipError_t e = few_front<T>(f, xq, a.H, xs, sets, cap, list, st);
     if (e != hipSuccess) return e;
     FewDownParams d{};
-    d.h = h; d.hq = hq; d.hs = hs; d.M = (int)a.M; d.I = (int)a.I; d.ids = a.ids; d.gw = a.gw; d.E = (int)a.E;
+    d.h = h; d.M = (int)a.M; d.I = (int)a.I; d.ids = a.ids; d.gw = a.gw; d.E = (int)a.E;
     d.topk = (int)a.topk; d.w = a.w2; d.ldw = a.ldw2; d.H = a.H; d.ws = a.s2; d.y = a.y; d.ldy = a.ldy;
-    if (few_quantise(P, a.I)) return run_down<T, kFewQuantise>(d, st);
-    e = quantise(T, h, a.I, P, a.I, hq, a.I, hs, a.ids, a.E, st);
+    if (few_quantise(P, a.I)) return run_down<T, kFewQuantise>(d, sets, st);
+    FewPrepParams q{};
+    q.x = h; q.ldx = a.I; q.rows = (int)P; q.K = (int)a.I; q.xq = hq; q.ldxq = a.I; q.xs = hs; q.pairs = true; q.M = (int)a.M;
+    q.E = (int)a.E; q.topk = (int)a.topk; q.cap = cap; q.ids = a.ids; q.gw = a.gw;
+    q.list = few_quantise(a.M, a.H) ? list : nullptr;  // the front made its list for itself
+    e = run_prep<T>(q, st);
     if (e != hipSuccess) return e;
-    return run_down<T, kFewStaged>(d, st);
+    d.hq = hq;
+    d.hs = hs;
+    d.list = list;
+    return run_down<T, kFewStaged>(d, sets, st);
 }
 
 template <int T>
@@ -266,7 +278,7 @@ hipError_t moe(const I8MoeArgs& a, hipStream_t st) {
     float *xs = (float*)(ws + r.xs), *hs = (float*)(ws + r.hs), *part = (float*)(ws + r.part);
     uint16_t* h = (uint16_t*)(ws + r.h);
     int32_t *offs = (int32_t*)(ws + r.offs), *toffs = (int32_t*)(ws + r.toffs), *perm = (int32_t*)(ws + r.perm);
-    if (few_fits(a.M, a.H)) return few_moe<T>(a, h, xq, xs, hq, hs, st);
+    if (few_fits(a.M, a.H)) return few_moe<T>(a, h, xq, xs, hq, hs, (FewList*)(ws + r.list), st);
     hipError_t e = a.logits ? route(a, st) : hipSuccess;
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(i8_sort_kernel, dim3(1), dim3(1024), 0, st, a.ids, (int)P, (int)a.E, kI8Bm, offs, toffs, perm);
@@ -298,7 +310,7 @@ hipError_t glu(const I8GluArgs& a, hipStream_t st) {
         FewFrontParams f{};
         f.x = a.x; f.ldx = a.ldx; f.M = (int)a.M; f.K = (int)a.K; f.w = a.w13; f.ldw = a.ldw; f.I = a.I; f.ws = a.s13;
         f.ws_step = a.ws_step; f.act = a.act; f.y = a.y; f.ldy = a.ldy;
-        return few_front<T>(f, a.xq, a.ldxq, a.xs, st);
+        return few_front<T>(f, a.xq, a.ldxq, a.xs, few_sets(a.M, 0, 0), 0, nullptr, st);
     }
     const hipError_t e = quantise(T, a.x, a.ldx, a.M, a.K, a.xq, a.ldxq, a.xs, nullptr, 0, st);
     if (e != hipSuccess) return e;

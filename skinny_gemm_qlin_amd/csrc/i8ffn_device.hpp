@@ -65,6 +65,39 @@ __device__ __forceinline__ uint2 codes8(const u32x4_t& v, double r) {
     return make_uint2(packed[0], packed[1]);
 }
 
+// A workgroup of NT threads quantises a row: largest magnitude, then codes.
+template <int T, int NT>
+__device__ __forceinline__ void quantise_row_wg(const uint16_t* row, int64_t K, int8_t* out, float* scale) {
+    constexpr int W = NT / 64, CACHED = 2;
+    __shared__ uint32_t part[W];
+    const int tid = threadIdx.x;
+    const int64_t nvec = K >> 3;
+    u32x4_t cache[CACHED];
+    uint32_t a = 0;
+#pragma unroll
+    for (int c = 0; c < CACHED; ++c) {
+        const int64_t i = tid + c * NT;
+        cache[c] = i < nvec ? ld16(row + i * 8) : u32x4_t{0, 0, 0, 0};
+        a = mag8(cache[c], a);
+    }
+    for (int64_t i = tid + CACHED * NT; i < nvec; i += NT) a = mag8(ld16(row + i * 8), a);
+    a = wave_mag(a);
+    if ((tid & 63) == 0) part[tid >> 6] = a;
+    __syncthreads();
+    uint32_t mag = part[0];
+#pragma unroll
+    for (int q = 1; q < W; ++q) mag = part[q] > mag ? part[q] : mag;
+    double r;
+    const float s = row_scale<T>(mag, r);
+    if (tid == 0) *scale = s;
+#pragma unroll
+    for (int c = 0; c < CACHED; ++c) {
+        const int64_t i = tid + c * NT;
+        if (i < nvec) *(uint2*)(out + i * 8) = codes8<T>(cache[c], r);
+    }
+    for (int64_t i = tid + CACHED * NT; i < nvec; i += NT) *(uint2*)(out + i * 8) = codes8<T>(ld16(row + i * 8), r);
+}
+
 // act(g) u of the int32 sums of a gate and an up row
 __device__ __forceinline__ float gated(int ag, int au, float xs, float sg, float su, int act) {
     float a, da;
@@ -117,7 +150,11 @@ template <int NR>
 __device__ __forceinline__ void route_token(const float* row, int E, int topk, int route, int lane, int& id, float& w) {
     uint32_t key[NR];
 #pragma unroll
-    for (int i = 0; i < NR; ++i) key[i] = i * 64 + lane < E ? route_key(row[i * 64 + lane]) : 0u;
+    for (int i = 0; i < NR; ++i) {
+        const int e = i * 64 + lane;
+        const float l = row[e < E ? e : E - 1];  // no load under a branch: all are on their way at once
+        key[i] = e < E ? route_key(l) : 0u;
+    }
     uint32_t all[NR];
 #pragma unroll
     for (int i = 0; i < NR; ++i) all[i] = key[i];

@@ -26,69 +26,111 @@
 namespace qlin {
 
 constexpr int kFewPairs = 256;   // 16 tokens, 16 slots
-constexpr int kFewThreads = 512, kFewWaves = kFewThreads / 64;
+constexpr int kFewThreads = 512, kFewWaves = kFewThreads / 64;  // one workgroup a compute unit
 constexpr int kFewTokens = 16;   // tokens of a chunk: four columns sets
 
 typedef int i32x4f_t __attribute__((ext_vector_type(4)));
 
+// x / d for 0 <= x < 2^24, r = 1 / d to within an ulp or two: the quotient of the floats is at most one off.
+__device__ __forceinline__ int few_div(int x, int d, float r) {
+    int q = (int)((float)x * r);
+    q -= q * d > x ? 1 : 0;
+    return q + ((q + 1) * d <= x ? 1 : 0);
+}
+
 // Pairs by expert, in chunks of up to `cap` pairs of one expert (at most kFewTokens).
 struct FewList {
-    int chunks;
+    int chunks, pad[3];
     int expert[kFewPairs], first[kFewPairs], count[kFewPairs];  // of each chunk
-    int pair[kFewPairs];                                        // pairs in expert order, pair order inside
+    int pair[kFewPairs], token[kFewPairs];                      // pairs in expert order, pair order inside; their tokens
 };
 
-// Built by a whole workgroup from the pairs' experts (ids outside [0, E) are in no chunk).  Every thread owns a
-// pair and counts those ahead of it: pairs of lower experts, and earlier ones of its own.  Opens and ends with a
-// barrier; sid keeps each pair's expert, -1 where it has none.
-__device__ __forceinline__ void few_list(FewList& l, int* sid, int npairs, const int32_t* ids, int E, int cap) {
-    const int tid = threadIdx.x;
-    int e = -1;
-    if (tid < npairs) {
-        e = ids[tid];
-        e = (uint32_t)e < (uint32_t)E ? e : -1;
-    }
-    if (tid < kFewPairs) sid[tid] = e;
-    if (tid == 0) l.chunks = 0;
-    w4_lds_barrier();
-    int lower = 0, before = 0, all = 0, heads = 0;
-    if (tid < npairs) {
-        typedef int i32x4l_t __attribute__((ext_vector_type(4)));
-#pragma unroll 4
-        for (int q = 0; q < npairs; q += 4) {
-            const i32x4l_t o = *(const i32x4l_t*)(sid + q);  // -1 past npairs
+struct FewListTemp {
+    int sid[kFewPairs];  // each pair's expert, -1 where it has none
+    int meta[kFewPairs];
+    int heads[4];
+};
+
+// Built by a whole workgroup from t.sid (-1 from npairs up to a multiple of 8; ready behind a barrier).  A pair's
+// place is the number of pairs ahead of it, of lower experts and earlier ones of its own; two or four lanes count
+// them.  Ends with a barrier.
+__device__ __forceinline__ void few_list(FewList& l, FewListTemp& t, int npairs, int topk, int cap) {
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+    typedef int i32x4l_t __attribute__((ext_vector_type(4)));
+    const int sh = npairs <= kFewThreads / 4 ? 2 : 1, pr = tid >> sh, part = tid & ((1 << sh) - 1);
+    const int e = pr < npairs ? t.sid[pr] : -1;
+    int lower = 0, before = 0, all = 0;
+    if (pr < npairs) {
+#pragma unroll 2
+        for (int q = part * 4; q < npairs; q += 4 << sh) {
+            const i32x4l_t o = *(const i32x4l_t*)(t.sid + q);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 lower += (uint32_t)o[i] < (uint32_t)e ? 1 : 0;  // as unsigned, -1 is never lower
-                before += (o[i] == e && q + i < tid) ? 1 : 0;
+                before += (o[i] == e && q + i < pr) ? 1 : 0;
                 all += o[i] == e ? 1 : 0;
             }
         }
-        if (e >= 0) {
-            l.pair[lower + before] = tid;
-            if (before == 0) l.first[lower] = all;  // for now: at the place of its first pair an expert's count
-        }
+    }
+    // over the pair's lanes: quad_perm 1 0 3 2, then 2 3 0 1
+    lower += dpp_mov<0xB1>(lower);
+    before += dpp_mov<0xB1>(before);
+    all += dpp_mov<0xB1>(all);
+    if (sh == 2) {
+        lower += dpp_mov<0x4E>(lower);
+        before += dpp_mov<0x4E>(before);
+        all += dpp_mov<0x4E>(all);
+    }
+    if (tid < kFewPairs) t.meta[tid] = -1;
+    w4_lds_barrier();
+    if (e >= 0 && part == 0) {
+        const int at = lower + before;
+        l.pair[at] = pr;
+        l.token[at] = few_div(pr, topk, __builtin_amdgcn_rcpf((float)topk));
+        t.meta[at] = before | all << 16;
     }
     w4_lds_barrier();
-    const bool head = e >= 0 && before == 0;
+    const int m = tid < kFewPairs ? t.meta[tid] : -1, b4 = m & 0xFFFF, cnt = m >> 16;
+    const bool head = m >= 0 && b4 - few_div(b4, cap, __builtin_amdgcn_rcpf((float)cap)) * cap == 0;
+    const uint64_t hm = __ballot(head);
+    if (tid < kFewPairs && lane == 0) t.heads[wv] = __popcll(hm);
+    w4_lds_barrier();
     if (head) {
-        for (int at = 0; at < lower;) {  // chunks of the experts ahead
-            const int n = l.first[at];
-            heads += (n + cap - 1) / cap;
-            at += n;
+        int c = __popcll(hm & ((1ull << lane) - 1ull));
+        for (int q = 0; q < wv; ++q) c += t.heads[q];
+        l.expert[c] = t.sid[l.pair[tid]];
+        l.first[c] = tid;
+        l.count[c] = cnt - b4 < cap ? cnt - b4 : cap;
+    }
+    if (tid == 0) l.chunks = t.heads[0] + t.heads[1] + t.heads[2] + t.heads[3];
+    w4_lds_barrier();
+}
+
+__device__ __forceinline__ void few_sid(FewListTemp& t, int npairs, const int32_t* ids, int E) {
+    if (threadIdx.x < kFewPairs) {
+        const int e = (int)threadIdx.x < npairs ? ids[threadIdx.x] : -1;
+        t.sid[threadIdx.x] = (uint32_t)e < (uint32_t)E ? e : -1;
+    }
+}
+
+// One workgroup: routes the tokens and leaves the pairs' experts in sid (before a barrier of the caller's).
+template <int NR>
+__device__ __forceinline__ void few_route(const float* logits, int64_t ldl, int M, int E, int topk, int route, int32_t* ids,
+                                          float* gw, bool store, FewListTemp& t) {
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, npairs = M * topk;
+    if (npairs + threadIdx.x < kFewPairs && threadIdx.x < 8) t.sid[npairs + threadIdx.x] = -1;
+    for (int m = wv; m < M; m += kFewWaves) {
+        int id;
+        float w;
+        route_token<NR>(logits + m * ldl, E, topk, route, lane, id, w);
+        if (lane < topk) {
+            t.sid[m * topk + lane] = id;
+            if (store) {
+                ids[m * topk + lane] = id;
+                gw[m * topk + lane] = w;
+            }
         }
     }
-    w4_lds_barrier();
-    if (head) {
-        const int n = (all + cap - 1) / cap;
-        for (int c = 0; c < n; ++c) {
-            l.expert[heads + c] = e;
-            l.first[heads + c] = lower + c * cap;
-            l.count[heads + c] = all - c * cap < cap ? all - c * cap : cap;
-        }
-        atomicMax(&l.chunks, heads + n);
-    }
-    w4_lds_barrier();
 }
 
 // sum over the 16 blocks: lanes of equal lane % 4; every lane gets it
@@ -113,42 +155,58 @@ enum FewSrc { kFewQuantise = 0, kFewStaged = 1 };
 
 // A workgroup quantises up to kFewUnits x 512 elements into its LDS: a unit is 512 elements of one row, one load a
 // lane.  The loads are issued by the constructor, long before their use.
-constexpr int kFewUnitsPerWave = 8, kFewUnits = kFewUnitsPerWave * kFewWaves;
+constexpr int kFewUnitsPerWave = 6, kFewUnits = kFewUnitsPerWave * kFewWaves;
 
 template <int T>
 struct FewQuantiser {
     u32x4_t v[kFewUnitsPerWave];
-    int rows, K, segs, lane, wv;
+    int rows, K, segs, units, lane, wv;
+    float rseg;
 
     __device__ FewQuantiser(const uint16_t* x, int64_t ldx, int rows_, int K_)
-        : rows(rows_), K(K_), segs((K_ + 511) >> 9), lane(threadIdx.x & 63),
-          wv(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) {
+        : rows(rows_), K(K_), segs((K_ + 511) >> 9), units(rows_ * segs), lane(threadIdx.x & 63),
+          wv(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), rseg(__builtin_amdgcn_rcpf((float)segs)) {
 #pragma unroll
         for (int i = 0; i < kFewUnitsPerWave; ++i) {
-            const int u = wv + i * kFewWaves, m = u / segs, k = (u - m * segs) * 512 + lane * 8;
-            v[i] = u < rows * segs && k < K ? ld16(x + m * ldx + k) : u32x4_t{0, 0, 0, 0};
+            v[i] = u32x4_t{0, 0, 0, 0};
+            if (i * kFewWaves + wv >= units) break;  // uniform
+            int m, seg;
+            where(i, m, seg);
+            const int k = seg * 512 + lane * 8;
+            if (k < K) v[i] = ld16(x + m * ldx + k);
         }
+    }
+    __device__ void where(int i, int& m, int& seg) const {
+        const int u = i * kFewWaves + wv;
+        m = __builtin_amdgcn_readfirstlane(few_div(u, segs, rseg));
+        seg = u - m * segs;
     }
     // mag: one zeroed word a row
     __device__ void maxima(uint32_t* mag) const {
 #pragma unroll
         for (int i = 0; i < kFewUnitsPerWave; ++i) {
-            const int u = wv + i * kFewWaves;
-            if (u >= rows * segs) break;  // uniform
-            const uint32_t m = wave_mag(mag8(v[i], 0));
-            if (lane == 0) atomicMax(&mag[u / segs], m);
+            if (i * kFewWaves + wv >= units) break;  // uniform
+            int m, seg;
+            where(i, m, seg);
+            const uint32_t a = wave_mag(mag8(v[i], 0));
+            if (lane == 0) atomicMax(&mag[m], a);
         }
     }
     // after a barrier; zeros from K to the pitch
     __device__ void codes(const uint32_t* mag, int8_t* out, float* scale, int pitch) const {
+        int last = -1;
+        double r = 0.0;
 #pragma unroll
         for (int i = 0; i < kFewUnitsPerWave; ++i) {
-            const int u = wv + i * kFewWaves;
-            if (u >= rows * segs) break;  // uniform
-            const int m = u / segs, seg = u - m * segs, k = seg * 512 + lane * 8;
-            double r;
-            const float s = row_scale<T>(mag[m], r);
-            if (seg == 0 && lane == 0) scale[m] = s;
+            if (i * kFewWaves + wv >= units) break;  // uniform
+            int m, seg;
+            where(i, m, seg);
+            const int k = seg * 512 + lane * 8;
+            if (m != last) {  // uniform
+                const float s = row_scale<T>(mag[m], r);
+                if (lane == 0) scale[m] = s;  // every wave of the row writes the same
+                last = m;
+            }
             if (k < pitch) *(uint2*)(out + m * pitch + k) = codes8<T>(v[i], r);  // past K: zeros give zeros
         }
         const int done = segs * 512;  // the rest of the ring's turn
@@ -157,122 +215,208 @@ struct FewQuantiser {
     }
 };
 
-// Copies code rows (row r is xq's row of[r], or r) to LDS.
+__device__ const u32x4_t kFewZero16 = {0u, 0u, 0u, 0u};
+
+// Copies code rows (row r is xq's row of[r], or r) to LDS, 1 KB a load instruction, zeros past K; the caller waits.
 __device__ __forceinline__ void stage_codes(const int8_t* xq, int64_t ldxq, const int* of, int rows, int K, int pitch,
                                             int8_t* out) {
-    const int per = pitch / 16, total = rows * per;
-    for (int i0 = threadIdx.x; i0 < total; i0 += 8 * kFewThreads) {
-        u32x4_t v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int i = i0 + j * kFewThreads, m = i / per, k = (i - m * per) * 16;
-            v[j] = i < total && k < K ? ld16(xq + (of ? of[m] : m) * ldxq + k) : u32x4_t{0, 0, 0, 0};
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int i = i0 + j * kFewThreads, m = i / per, k = (i - m * per) * 16;
-            if (i < total) *(u32x4_t*)(out + m * pitch + k) = v[j];
-        }
+    const int lane = threadIdx.x & 63;
+    for (int r = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); r < rows; r += kFewWaves) {
+        const int8_t* src = xq + (of ? __builtin_amdgcn_readfirstlane(of[r]) : r) * ldxq + lane * 16;
+        for (int k = 0; k < K; k += 1024)
+            __builtin_amdgcn_global_load_lds(k + lane * 16 < K ? (const void*)(src + k) : (const void*)&kFewZero16,
+                                             (lds_void_t*)(out + r * pitch + k), 16, 0, 0);
     }
 }
 
-// What a wave has requested: the first kFewDepth steps of its item, and the item's channel scales.  The ring is
-// always full: the steps past an item's end are the next item's first.
+// Everything but this wave's last N loads (its ring's) is there; behind the barrier what the others loaded into LDS, too.
+template <int N>
+__device__ __forceinline__ void few_staged_barrier() {
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt((N & 15) | 0x70);  // vmcnt(N) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+// What a wave has requested: kFewDepth steps (a turn) of its item, and the item's channel scales.  The ring is always
+// full: behind an item's last turn follows the next item's first.
 struct FewRing {
     u32x4_t w[kFewDepth];
     f32x2v_t sc;
     const int8_t* wp;
 
-    __device__ void prime(const int8_t* row, int K) {
+    __device__ void prime(const int8_t* row, int turn, int K) {
         const int at = ((threadIdx.x & 63) >> 2) * 16;
         wp = row;
 #pragma unroll
         for (int u = 0; u < kFewDepth; ++u) {
-            const int k = u * 256 + at;
+            const int k = (turn * kFewDepth + u) * 256 + at;
             w[u] = ld_stream(wp + (k < K ? k : 0));  // past K: any of the row, against zero codes
         }
     }
 };
 
-// One item: its sums with NS x 4 columns, cb[n] the code row (LDS, zeros past K) of this lane's token of set n.
+// Turns [t, end) of an item, at least one: its sums with NS x 4 columns, cb[n] the code row (LDS, zeros past K) of this
+// lane's token of set n.
 template <int NS>
-__device__ __forceinline__ void few_item(FewRing& ring, const int8_t* next, int K, const int8_t* const (&cb)[4],
-                                         i32x4f_t (&acc)[4]) {
+__device__ __forceinline__ void few_item(FewRing& ring, const int8_t* next, int t, int end, int K,
+                                         const int8_t* const (&cb)[NS], i32x4f_t (&acc)[NS]) {
     constexpr int D = kFewDepth;
     const int at = ((threadIdx.x & 63) >> 2) * 16;
-    const int turns = (K + 256 * D - 1) / (256 * D);
 #pragma unroll
     for (int n = 0; n < NS; ++n) acc[n] = i32x4f_t{0, 0, 0, 0};
-    for (int t = 0; t < turns; ++t) {
+    do {
         int k0 = (t + 1) * 256 * D;  // of the ring's next turn
-        if (t + 1 == turns) {
+        if (t + 1 == end) {
             k0 = 0;
             ring.wp = next;
         }
+        u32x4_t x[2][NS];  // codes of this step and the next
+#pragma unroll
+        for (int n = 0; n < NS; ++n) x[0][n] = *(const u32x4_t*)(cb[n] + t * D * 256 + at);
 #pragma unroll
         for (int u = 0; u < D; ++u) {
-            u32x4_t x[NS];
+            if (u + 1 < D) {
 #pragma unroll
-            for (int n = 0; n < NS; ++n) x[n] = *(const u32x4_t*)(cb[n] + (t * D + u) * 256 + at);
+                for (int n = 0; n < NS; ++n) x[(u + 1) & 1][n] = *(const u32x4_t*)(cb[n] + (t * D + u + 1) * 256 + at);
+            }
 #pragma unroll
             for (int d = 0; d < 4; ++d)
 #pragma unroll
                 for (int n = 0; n < NS; ++n)
-                    acc[n] = __builtin_amdgcn_mfma_i32_4x4x4i8((int)ring.w[u][d], (int)x[n][d], acc[n], 0, 0, 0);
+                    acc[n] = __builtin_amdgcn_mfma_i32_4x4x4i8((int)ring.w[u][d], (int)x[u & 1][n][d], acc[n], 0, 0, 0);
             const int k = k0 + u * 256 + at;
             ring.w[u] = ld_stream(ring.wp + (k < K ? k : 0));
+            __builtin_amdgcn_sched_barrier(0);  // or the turn's loads are all issued at its end, when nothing is in flight
         }
-    }
+    } while (++t < end);
 #pragma unroll
     for (int n = 0; n < NS; ++n)
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[n][r] = blocks_sum(acc[n][r]);
 }
 
-// A wave's items [item, stop) of a list of chunks x `per` items.  enter(c): the chunk's weights; row(i), scales(i): the
-// row that this lane loads of item i of the chunk entered last, and its channel scales; tokens(c, cb): looks up
-// chunk c's tokens and returns their number; done(i, acc, sc).  The next item's rows are requested, and its scales,
-// while this one is multiplied, across chunks too.
-struct FewWork {
-    int item, stop, per, c, i;
+// first of share `me`, where every share has q and the first r one more
+__device__ __forceinline__ int few_first(int q, int r, int me) { return me * q + (me < r ? me : r); }
 
+// Sums of the items that more than one wave had turns of: [wave that had its first turn][token][row], zeroed ahead.
+typedef int FewSlots[kFewWaves][kFewTokens][4];
+
+// A workgroup's items, chunks x `per` of them, are dealt to its waves by turns of 1024 K: every wave has as many as
+// any other, to one.  An item that lies on the border of two waves is joined in LDS, in whole numbers.
+//   enter(c): the chunk's weights; row(i), scales(i): the row that this lane loads of item i of the chunk entered
+//   last, and its channel scales; tokens(c, cb): looks up chunk c's tokens;
+//   done(i, acc, sc).
+template <int NS>
+struct FewWork {
+    int per, turns, q, r;      // items a chunk, turns an item; turns a wave, and how many waves have one more
+    int c, i, t, left;         // chunk, item in it, turn of it; turns that are left
+    int open_c, open_i;        // an item whose first turn was this wave's and whose last was not (open_c < 0: none)
+
+    // items [first, first + items) of all
     template <class Enter, class Row, class Scales>
-    __device__ void prime(FewRing& ring, int K, const Enter& enter, const Row& row, const Scales& scales) {
-        if (item >= stop) return;
-        c = item / per;
-        i = item - c * per;
+    __device__ void prime(FewRing& ring, int first, int items, int wave, int K, const Enter& enter, const Row& row,
+                          const Scales& scales) {
+        turns = (K + 256 * kFewDepth - 1) / (256 * kFewDepth);
+        q = items * turns / kFewWaves;
+        r = items * turns % kFewWaves;
+        const int at = few_first(q, r, wave);
+        left = q + (wave < r ? 1 : 0);
+        int it = few_div(at, turns, __builtin_amdgcn_rcpf((float)turns));
+        t = at - it * turns;
+        it = left > 0 ? first + it : first;  // without turns: any item, so that the loads are the same on all paths
+        c = __builtin_amdgcn_readfirstlane(few_div(it, per, __builtin_amdgcn_rcpf((float)per)));
+        i = __builtin_amdgcn_readfirstlane(it - c * per);
+        t = __builtin_amdgcn_readfirstlane(left > 0 ? t : 0);
+        left = __builtin_amdgcn_readfirstlane(left);
+        open_c = -1;
+        open_i = 0;
         enter(c);
         ring.sc = scales(i);
-        ring.prime(row(i), K);
+        ring.prime(row(i), t, K);
     }
     template <class Enter, class Row, class Scales, class Tokens, class Done>
-    __device__ void run(FewRing& ring, int K, const Enter& enter, const Row& row, const Scales& scales,
-                        const Tokens& tokens, const Done& done) {
-        const int8_t* cb[4];
-        int at = -1, cnt = 0;
-        for (; item < stop; ++item) {
-            if (c != at) cnt = tokens(c, cb);
+    __device__ void run(FewRing& ring, int wave, int K, FewSlots& slots, const Enter& enter, const Row& row,
+                        const Scales& scales, const Tokens& tokens, const Done& done) {
+        const int8_t* cb[NS];
+        const int lane = threadIdx.x & 63;
+        int at = -1;
+        while (left > 0) {
+            if (c != at) tokens(c, cb);
             at = c;
-            const int here = i;
-            if (item + 1 < stop && ++i == per) {  // past the end: this item's rows, again
+            const int here = i, t0 = t, end = turns - t < left ? turns : t + left;
+            left -= end - t0;
+            if (left > 0 && ++i == per) {  // past the end: this item's rows, again
                 i = 0;
                 enter(++c);
             }
+            t = 0;
             const int8_t* next = row(i);
             const f32x2v_t sc = scales(i);
-            i32x4f_t acc[4];
-            if (cnt <= 4) few_item<1>(ring, next, K, cb, acc);
-            else if (cnt <= 8) few_item<2>(ring, next, K, cb, acc);
-            else few_item<4>(ring, next, K, cb, acc);
-            done(here, acc, ring.sc);
+            i32x4f_t acc[NS];
+            few_item<NS>(ring, next, t0, end, K, cb, acc);
+            if (t0 == 0 && end == turns) {
+                done(here, acc, ring.sc);
+            } else {
+                int home = wave;
+                if (t0 > 0) {  // the wave that has the item's first turn
+                    const int tau = few_first(q, r, wave) - t0, big = r * (q + 1);
+                    home = tau < big ? few_div(tau, q + 1, __builtin_amdgcn_rcpf((float)(q + 1)))
+                                     : r + few_div(tau - big, q, __builtin_amdgcn_rcpf((float)q));
+                } else {
+                    open_c = at;
+                    open_i = here;
+                }
+                if (lane < 4)
+#pragma unroll
+                    for (int s = 0; s < NS; ++s)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) atomicAdd(&slots[home][s * 4 + lane][k], acc[s][k]);
+            }
             ring.sc = sc;
         }
     }
+    // behind a barrier: the item that the wave had the first turn of
+    template <class Enter, class Scales, class Tokens, class Done>
+    __device__ void close(int wave, FewSlots& slots, const Enter& enter, const Scales& scales, const Tokens& tokens,
+                          const Done& done) {
+        if (open_c < 0) return;
+        const int8_t* cb[NS];
+        i32x4f_t acc[NS];
+        tokens(open_c, cb);
+        enter(open_c);
+#pragma unroll
+        for (int s = 0; s < NS; ++s) acc[s] = *(const i32x4f_t*)slots[wave][s * 4 + (threadIdx.x & 3)];
+        done(open_i, acc, scales(open_i));
+    }
+};
+
+__device__ __forceinline__ void few_clear(FewSlots& slots) {
+    static_assert(sizeof(FewSlots) == kFewThreads * 4, "a word a thread");
+    ((int*)slots)[threadIdx.x] = 0;
+}
+
+// share `me` of `of` equal ones of n
+__device__ __forceinline__ void few_share(int n, int me, int of, int& first, int& count) {
+    const int q = few_div(n, of, __builtin_amdgcn_rcpf((float)of)), r = n - q * of;
+    first = __builtin_amdgcn_readfirstlane(few_first(q, r, me));
+    count = __builtin_amdgcn_readfirstlane(q + (me < r ? 1 : 0));
+}
+
+// Staged sources: a kernel ahead quantises the rows (tokens or pairs), a workgroup
+// a row, and one more workgroup routes and makes the list.
+struct FewPrepParams {
+    const uint16_t* x; int64_t ldx; int rows, K; int8_t* xq; int64_t ldxq; float* xs;
+    bool pairs;                                      // rows are pairs: those without an expert are left out
+    const float* logits; int64_t ldl; int M, E, topk, route, cap;
+    int32_t* ids; float* gw; FewList* list;          // the list: by workgroup `rows`, if there is one
 };
 
 struct FewFrontParams {
     const uint16_t* x; int64_t ldx;                  // quantise: 16-bit rows
-    const int8_t* xq; int64_t ldxq; const float* xs; // else: codes, scales
+    const int8_t* xq; int64_t ldxq; const float* xs; // staged: codes, scales
+    const FewList* list;                             // staged: of the pairs
     int8_t* xq_out; float* xs_out;                   // dense, quantise: the codes and scales go here too
     int M, K;
     const float* logits; int64_t ldl; int E, topk, route;  // E = 0: dense
@@ -281,13 +425,37 @@ struct FewFrontParams {
     uint16_t* y; int64_t ldy;                        // rows: pairs, or tokens where dense
 };
 
-// Workgroup b of G owns the items [b n / G, (b + 1) n / G) of all chunks' output
-// pairs, each wave a run of them.
-template <int T, int SRC, int NR>
-__global__ __launch_bounds__(kFewThreads, 4) void few_front_kernel(const FewFrontParams p) {
+__device__ __forceinline__ void few_copy_list(FewList& to, const FewList* from) {
+    for (int i = threadIdx.x; i < (int)(sizeof(FewList) / 16); i += kFewThreads)
+        ((u32x4_t*)&to)[i] = ((const u32x4_t*)from)[i];
+}
+
+template <int T, int NR>
+__global__ __launch_bounds__(kFewThreads) void few_prep_kernel(const FewPrepParams p) {
+    if ((int)blockIdx.x < p.rows) {
+        if (p.pairs && (uint32_t)p.ids[blockIdx.x] >= (uint32_t)p.E) return;
+        quantise_row_wg<T, kFewThreads>(p.x + blockIdx.x * p.ldx, p.K, p.xq + blockIdx.x * p.ldxq, p.xs + blockIdx.x);
+        return;
+    }
+    __shared__ __align__(16) FewList list;
+    __shared__ __align__(16) FewListTemp temp;
+    const int npairs = p.M * p.topk;
+    if (p.logits) few_route<NR>(p.logits, p.ldl, p.M, p.E, p.topk, p.route, p.ids, p.gw, true, temp);
+    else few_sid(temp, npairs, p.ids, p.E);
+    w4_lds_barrier();
+    few_list(list, temp, npairs, p.topk, p.cap);
+    for (int i = threadIdx.x; i < (int)(sizeof(FewList) / 16); i += kFewThreads)
+        ((u32x4_t*)p.list)[i] = ((const u32x4_t*)&list)[i];
+}
+
+// A workgroup owns a run of all chunks' items, two outputs each.
+// NR: only where the workgroup routes.
+template <int T, int SRC, int NS, int NR>
+__global__ __launch_bounds__(kFewThreads, 2) void few_front_kernel(const FewFrontParams p) {
     extern __shared__ __align__(16) uint8_t few_lds[];  // codes [M][pitch]
-    __shared__ FewList list;
-    __shared__ __align__(16) int sid[kFewPairs];
+    __shared__ __align__(16) FewList list;
+    __shared__ __align__(16) FewListTemp temp;
+    __shared__ __align__(16) FewSlots slots;
     __shared__ float scale[kFewTokens];
     __shared__ uint32_t mag[kFewTokens];
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -296,50 +464,46 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_front_kernel(const FewFron
     int8_t* codes = (int8_t*)few_lds;
     const int npairs = moe ? p.M * p.topk : p.M;
     FewQuantiser<T> quant(p.x, p.ldx, SRC == kFewQuantise ? p.M : 0, p.K);
-    if (tid < kFewTokens) mag[tid] = 0;
-    if (moe && p.logits) {
-        for (int m = wv; m < p.M; m += kFewWaves) {
-            int id;
-            float w;
-            route_token<NR>(p.logits + m * p.ldl, p.E, p.topk, p.route, lane, id, w);
-            if (lane < p.topk) {
-                list.pair[m * p.topk + lane] = id;  // not yet in use
-                if (blockIdx.x == 0) {
-                    p.ids[m * p.topk + lane] = id;
-                    p.gw[m * p.topk + lane] = w;
-                }
-            }
+    few_clear(slots);
+    if constexpr (SRC == kFewQuantise) {
+        if (tid < kFewTokens) mag[tid] = 0;
+        if (moe) {
+            if (p.logits) few_route<NR>(p.logits, p.ldl, p.M, p.E, p.topk, p.route, p.ids, p.gw, blockIdx.x == 0, temp);
+            else few_sid(temp, npairs, p.ids, p.E);
+        }
+        w4_lds_barrier();
+        if (moe) few_list(list, temp, npairs, p.topk, 4 * NS);
+    } else {
+        stage_codes(p.xq, p.ldxq, nullptr, p.M, p.K, pitch, codes);
+        if (tid < p.M) scale[tid] = p.xs[tid];
+        if (moe) {
+            few_copy_list(list, p.list);
+            w4_lds_barrier();
         }
     }
-    __syncthreads();
-    int chunks = 1;
-    if (moe) {
-        few_list(list, sid, npairs, p.logits ? (const int32_t*)list.pair : p.ids, p.E, kFewTokens);
-        chunks = __builtin_amdgcn_readfirstlane(list.chunks);
-    }
-    FewWork work;
-    work.per = (int)((p.I + 1) / 2);  // items of a chunk: two outputs
-    const int n = chunks * work.per, waves = gridDim.x * kFewWaves, me = blockIdx.x * kFewWaves + wv;
-    work.item = (int)((int64_t)n * me / waves);
-    work.stop = (int)((int64_t)n * (me + 1) / waves);
-    const int r4 = lane & 3, o = (lane >> 2) & 1;
+    const int chunks = moe ? __builtin_amdgcn_readfirstlane(list.chunks) : 1;
+    FewWork<NS> work;
+    work.per = (int)((p.I + 1) / 2);  // items of a chunk
+    int first_item, items;
+    few_share(chunks * work.per, blockIdx.x, gridDim.x, first_item, items);
+    const int r4 = lane & 3, o = (lane >> 2) & 1, I = (int)p.I;
     const int8_t* w = nullptr;
     const float* ws = nullptr;
     auto enter = [&](int c) {
-        const int e = moe ? __builtin_amdgcn_readfirstlane(list.expert[c]) : 0;
+        const int e = moe && chunks > 0 ? __builtin_amdgcn_readfirstlane(list.expert[c]) : 0;
         w = p.w + (int64_t)e * 2 * p.I * p.ldw;
         ws = p.ws + (int64_t)e * 2 * p.I * p.ws_step;
     };
     auto row = [&](int it) {  // gate rows of outputs 2 it and 2 it + 1, then their up rows
-        const int64_t i = 2 * (int64_t)it + (r4 & 1), ic = i < p.I ? i : p.I - 1;
-        return w + (ic + (r4 >> 1) * p.I) * p.ldw;
+        const int i = 2 * it + (r4 & 1), ic = i < I ? i : I - 1;
+        return w + (uint64_t)(uint32_t)(ic + (r4 >> 1) * I) * (uint32_t)p.ldw;
     };
     auto scales = [&](int it) {
-        const int64_t i = 2 * (int64_t)it + o, ic = i < p.I ? i : p.I - 1;
-        return f32x2v_t{ws[ic * p.ws_step], ws[(p.I + ic) * p.ws_step]};
+        const int i = 2 * it + o, ic = i < I ? i : I - 1;
+        return f32x2v_t{ws[ic * p.ws_step], ws[(I + ic) * p.ws_step]};
     };
     FewRing ring;
-    work.prime(ring, p.K, enter, row, scales);
+    work.prime(ring, items > 0 ? first_item : 0, items, wv, p.K, enter, row, scales);
     if constexpr (SRC == kFewQuantise) {
         quant.maxima(mag);
         w4_lds_barrier();
@@ -353,40 +517,40 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_front_kernel(const FewFron
             if (tid < p.M) p.xs_out[tid] = scale[tid];
         }
     } else {
-        if (tid < p.M) scale[tid] = p.xs[tid];
-        stage_codes(p.xq, p.ldxq, nullptr, p.M, p.K, pitch, codes);
-        w4_lds_barrier();
+        few_staged_barrier<kFewDepth>();
     }
-    int row_of[4], cnt = 0;
-    float xs[4];
-    auto tokens = [&](int c, const int8_t* (&cb)[4]) {
+    int row_of[NS], cnt = 0;
+    float xs[NS];
+    auto tokens = [&](int c, const int8_t* (&cb)[NS]) {
         cnt = moe ? __builtin_amdgcn_readfirstlane(list.count[c]) : p.M;
         const int first = moe ? list.first[c] : 0;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
+        for (int s = 0; s < NS; ++s) {
             const int j = s * 4 + r4 < cnt ? s * 4 + r4 : 0;
             row_of[s] = moe ? list.pair[first + j] : j;
-            const int t = moe ? row_of[s] / p.topk : j;
+            const int t = moe ? list.token[first + j] : j;
             cb[s] = codes + t * pitch;
             xs[s] = scale[t];
         }
-        return cnt;
     };
-    auto done = [&](int it, i32x4f_t (&acc)[4], const f32x2v_t& sc) {
-        const int64_t i = 2 * (int64_t)it + o;
-        if (lane >= 8 || i >= p.I) return;
+    auto done = [&](int it, i32x4f_t (&acc)[NS], const f32x2v_t& sc) {
+        const int i = 2 * it + o;
+        if (lane >= 8 || i >= I) return;
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+        for (int s = 0; s < NS; ++s)
             if (s * 4 + r4 < cnt)
                 p.y[row_of[s] * p.ldy + i] = f32_to_h<T>(gated(o ? acc[s][1] : acc[s][0], o ? acc[s][3] : acc[s][2], xs[s],
                                                                sc[0], sc[1], p.act));
     };
-    work.run(ring, p.K, enter, row, scales, tokens, done);
+    work.run(ring, wv, p.K, slots, enter, row, scales, tokens, done);
+    w4_lds_barrier();
+    work.close(wv, slots, enter, scales, tokens, done);
 }
 
 struct FewDownParams {
     const uint16_t* h;                              // quantise: [P][I]
-    const int8_t* hq; const float* hs;              // else: codes [P][I], scales
+    const int8_t* hq; const float* hs;              // staged: codes [P][I], scales
+    const FewList* list;                            // staged: in chunks of at most `rows` pairs
     int M, I;
     const int32_t* ids; const float* gw; int E, topk;
     const int8_t* w; int64_t ldw; int64_t H; const float* ws;
@@ -398,11 +562,12 @@ struct FewDownParams {
 // Workgroup b of G owns a run of the output's 4-row groups and takes all
 // experts through it, so the slots are joined in LDS, in slot order.  Where LDS
 // does not hold all pairs' codes, the chunks are taken in batches that it holds.
-template <int T, int SRC>
-__global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(const FewDownParams p) {
+template <int T, int SRC, int NS>
+__global__ __launch_bounds__(kFewThreads, 2) void few_down_kernel(const FewDownParams p) {
     extern __shared__ __align__(16) uint8_t few_lds[];  // sums [block][P][4], then codes [rows][pitch]
-    __shared__ FewList list;
-    __shared__ __align__(16) int sid[kFewPairs];
+    __shared__ __align__(16) FewList list;
+    __shared__ __align__(16) FewListTemp temp;
+    __shared__ __align__(16) FewSlots slots;
     __shared__ float scale[kFewPairs];
     __shared__ uint32_t mag[kFewPairs];
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -410,26 +575,36 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(const FewDownP
     float* sums = (float*)few_lds;
     int8_t* codes = (int8_t*)few_lds + (size_t)p.block * npairs * 16;
     FewQuantiser<T> quant(p.h, p.I, SRC == kFewQuantise ? npairs : 0, p.I);
-    if (tid < kFewPairs) mag[tid] = 0;
-    few_list(list, sid, npairs, p.ids, p.E, p.rows < kFewTokens ? p.rows : kFewTokens);
+    few_clear(slots);
+    few_sid(temp, npairs, p.ids, p.E);
+    if constexpr (SRC == kFewQuantise) {
+        if (tid < kFewPairs) mag[tid] = 0;
+        w4_lds_barrier();
+        few_list(list, temp, npairs, p.topk, 4 * NS);
+    } else {
+        few_copy_list(list, p.list);
+        w4_lds_barrier();
+    }
     const int chunks = __builtin_amdgcn_readfirstlane(list.chunks);
     const int groups = (int)(p.H / 4);
-    const int g0 = (int)((int64_t)groups * blockIdx.x / gridDim.x), g1 = (int)((int64_t)groups * (blockIdx.x + 1) / gridDim.x);
+    FewWork<NS> work;
+    int g0, g1;
+    few_share(groups, blockIdx.x, gridDim.x, g0, g1);
+    g1 += g0;
     const int r4 = lane & 3;
     // the block of row groups, and the batch of chunks [c0, c1) with pairs from list.pair[base], that are worked on
     int gb = g0, nb = 0, c0 = 0, c1 = 0, base = 0, pairs = 0;
     const int8_t* w = nullptr;
     const float* ws = nullptr;
-    auto row = [&](int it) { return w + (int64_t)4 * it * p.ldw; };
+    auto row = [&](int it) { return w + (uint64_t)(uint32_t)(4 * it) * (uint32_t)p.ldw; };
     auto scales = [&](int it) { return f32x2v_t{ws[4 * it], 0.f}; };
     auto enter = [&](int c) {
-        const int e = __builtin_amdgcn_readfirstlane(list.expert[c0 + c]);
+        const int e = c1 > c0 ? __builtin_amdgcn_readfirstlane(list.expert[c0 + c]) : 0;
         w = p.w + ((int64_t)e * p.H + 4 * gb + r4) * p.ldw;
         ws = p.ws + (int64_t)e * p.H + 4 * gb + ((lane >> 2) & 3);
     };
     FewRing ring;
-    FewWork work;
-    auto open_batch = [&]() {  // from chunk c0; its weights are requested
+    auto open_batch = [&](bool restage) {  // from chunk c0: its codes are copied and its first weights requested
         nb = g1 - gb < p.block ? g1 - gb : p.block;
         c1 = c0;
         base = c0 < chunks ? __builtin_amdgcn_readfirstlane(list.first[c0]) : 0;
@@ -441,69 +616,66 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_down_kernel(const FewDownP
             ++c1;
         }
         work.per = nb;
-        const int n = (c1 - c0) * nb;
-        work.item = n * wv / kFewWaves;
-        work.stop = n * (wv + 1) / kFewWaves;
-        work.prime(ring, p.I, enter, row, scales);
+        if (SRC == kFewStaged && restage) stage_codes(p.hq, p.I, list.pair + base, pairs, p.I, pitch, codes);
+        work.prime(ring, 0, (c1 - c0) * nb, wv, p.I, enter, row, scales);
     };
-    auto stage = [&]() { stage_codes(p.hq, p.I, list.pair + base, pairs, p.I, pitch, codes); };
-    open_batch();
+    if constexpr (SRC == kFewStaged)
+        if (tid < npairs && temp.sid[tid] >= 0) scale[tid] = p.hs[tid];
+    open_batch(true);
     if constexpr (SRC == kFewQuantise) {
         quant.maxima(mag);
         w4_lds_barrier();
         quant.codes(mag, codes, scale, pitch);
+        w4_lds_barrier();
     } else {
-        if (tid < npairs && sid[tid] >= 0) scale[tid] = p.hs[tid];
-        stage();
+        few_staged_barrier<kFewDepth>();
     }
-    w4_lds_barrier();
-    int pair[4], cnt = 0;
-    float hs[4];
-    auto tokens = [&](int c, const int8_t* (&cb)[4]) {
+    int pair[NS], cnt = 0;
+    float hs[NS];
+    auto tokens = [&](int c, const int8_t* (&cb)[NS]) {
         cnt = __builtin_amdgcn_readfirstlane(list.count[c0 + c]);
         const int first = list.first[c0 + c];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
+        for (int s = 0; s < NS; ++s) {
             const int j = first + (s * 4 + r4 < cnt ? s * 4 + r4 : 0);
             pair[s] = list.pair[j];
             hs[s] = scale[pair[s]];
             cb[s] = codes + (SRC == kFewQuantise ? pair[s] : j - base) * pitch;
         }
-        return cnt;
     };
-    auto done = [&](int it, i32x4f_t (&acc)[4], const f32x2v_t& sc) {
+    auto done = [&](int it, i32x4f_t (&acc)[NS], const f32x2v_t& sc) {
         const int r = lane >> 2;
         if (r >= 4) return;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
+        for (int s = 0; s < NS; ++s) {
             const int a = r == 0 ? acc[s][0] : (r == 1 ? acc[s][1] : (r == 2 ? acc[s][2] : acc[s][3]));
             if (s * 4 + r4 < cnt) sums[(it * npairs + pair[s]) * 4 + r] = ((float)a * hs[s]) * sc[0];
         }
     };
     for (;;) {
-        work.run(ring, p.I, enter, row, scales, tokens, done);
-        w4_lds_barrier();  // everyone is done with the codes, and the batch's sums are there
+        work.run(ring, wv, p.I, slots, enter, row, scales, tokens, done);
+        w4_lds_barrier();  // everyone is done with the codes
+        work.close(wv, slots, enter, scales, tokens, done);
         const int gs = gb, ns = nb;
         const bool more = c1 < chunks, restage = more || c0 > 0;  // chunks of this block
         c0 = more ? c1 : 0;
         gb = more ? gb : gb + nb;
         const bool last = gb >= g1;
-        if (!last) {
-            open_batch();  // its first weights travel while the sums are joined
-            if (SRC == kFewStaged && restage) stage();
-        }
+        if (!last) open_batch(restage);  // its first weights travel while the sums are joined
+        w4_lds_barrier();  // the batch's sums are there
+        few_clear(slots);
         if (!more)
             for (int i = tid; i < p.M * ns * 4; i += kFewThreads) {
-                const int t = i / (ns * 4), r = i - t * ns * 4;  // r: row of the block
+                const int t = few_div(i, ns * 4, __builtin_amdgcn_rcpf((float)(ns * 4))), r = i - t * ns * 4;  // r: row of the block
                 float sum = 0.f;
                 for (int j = 0; j < p.topk; ++j) {
                     const int q = t * p.topk + j;
-                    if (sid[q] >= 0) sum = fmaf(p.gw[q], sums[((r >> 2) * npairs + q) * 4 + (r & 3)], sum);
+                    if (temp.sid[q] >= 0) sum = fmaf(p.gw[q], sums[((r >> 2) * npairs + q) * 4 + (r & 3)], sum);
                 }
                 p.y[t * p.ldy + 4 * gs + r] = f32_to_h<T>(sum);
             }
         if (last) break;
-        w4_lds_barrier();
+        few_staged_barrier<0>();
     }
 }
 
