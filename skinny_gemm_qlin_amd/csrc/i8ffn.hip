@@ -59,8 +59,7 @@ hipError_t route(const I8MoeArgs& a, hipStream_t st) {
 // computed on its own, the combine adds in slot order).
 constexpr int kI8MaxE = 1024;
 
-__global__ __launch_bounds__(1024) void i8_sort_kernel(const int32_t* ids, int P, int E, int bm, int32_t* offs,
-                                                       int32_t* toffs, int32_t* perm) {
+__device__ void sort_pairs(const int32_t* ids, int P, int E, int bm, int32_t* offs, int32_t* toffs, int32_t* perm) {
     __shared__ int32_t cnt[kI8MaxE], cur[kI8MaxE], wsum[16], wtile[16];
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
     cnt[tid] = 0;
@@ -105,6 +104,37 @@ __global__ __launch_bounds__(1024) void i8_sort_kernel(const int32_t* ids, int P
     }
 }
 
+// Workgroups ahead of the last quantise a token each; the last one sorts the
+// pairs and, NR > 0, routes the tokens first.
+struct I8PrepParams {
+    const uint16_t* x; int64_t ldx; int64_t M; int64_t K; int8_t* xq; float* xs;
+    const float* logits; int64_t ldl; int E, topk, route, bm;
+    int32_t* ids; float* gw; int32_t *offs, *toffs, *perm;
+};
+
+template <int T, int NR>
+__global__ __launch_bounds__(1024) void i8_prep_kernel(const I8PrepParams p) {
+    const int64_t m = blockIdx.x;
+    if (m < p.M) {
+        quantise_row_wg<T, 1024>(p.x + m * p.ldx, p.K, p.xq + m * p.K, p.xs + m);
+        return;
+    }
+    if constexpr (NR > 0) {
+        const int lane = threadIdx.x & 63;
+        for (int t = threadIdx.x >> 6; t < p.M; t += 16) {
+            int id;
+            float w;
+            route_token<NR>(p.logits + t * p.ldl, p.E, p.topk, p.route, lane, id, w);
+            if (lane < p.topk) {
+                p.ids[t * p.topk + lane] = id;
+                p.gw[t * p.topk + lane] = w;
+            }
+        }
+        __syncthreads();  // the ids are read back by other threads of this workgroup
+    }
+    sort_pairs(p.ids, (int)p.M * p.topk, p.E, p.bm, p.offs, p.toffs, p.perm);
+}
+
 // y[t,n] = r16(sum_j gw[t,j] part[t,j,n]) in slot order, four columns a thread.
 template <int T>
 __global__ __launch_bounds__(256) void i8_combine_kernel(const float* part, const int32_t* ids, const float* gw, int64_t M,
@@ -125,10 +155,13 @@ __global__ __launch_bounds__(256) void i8_combine_kernel(const float* part, cons
     for (int c = 0; c < 4; ++c) y[t * ldy + n + c] = f32_to_h<T>(sum[c]);
 }
 
+// columns [first, first + count) of the product with row_tiles tiles of BM rows (at most, where they are grouped)
 template <int T, int EPI, int BN, int BM, int WGN, int WGM>
-hipError_t run_gemm(const I8GemmParams& p, int64_t row_tiles, hipStream_t st) {
+hipError_t run_gemm(I8GemmParams p, int64_t row_tiles, int64_t first, int64_t count, hipStream_t st) {
     constexpr int CT = EPI == kI8Gated ? BN / 2 : BN;
-    const int64_t tiles = row_tiles * ((p.C + CT - 1) / CT);
+    p.c_first = first;
+    p.c_count = count;
+    const int64_t tiles = row_tiles * ((count + CT - 1) / CT);
     hipLaunchKernelGGL((i8_gemm_kernel<T, EPI, BN, BM, WGN, WGM>), dim3((unsigned)((tiles + 7) / 8 * 8)),
                        dim3(64 * WGN * WGM), 0, st, p);
     return hipGetLastError();
@@ -136,8 +169,6 @@ hipError_t run_gemm(const I8GemmParams& p, int64_t row_tiles, hipStream_t st) {
 
 // row tiles that P pairs of E groups can make at most
 int64_t most_tiles(int64_t P, int64_t E, int64_t bm) { return P / bm + (E < P ? E : P); }
-
-constexpr int kI8Bm = 64;
 
 struct MoeRegions { size_t xq, xs, h, hq, hs, part, offs, toffs, perm, list, total; };
 
@@ -165,29 +196,11 @@ MoeRegions regions(int64_t M, int64_t H, int64_t I, int64_t topk, int64_t E) {
 }
 
 // ---- up to 16 tokens
-constexpr int kFewLds = 146 * 1024;     // dynamic LDS next to the lists, of 160 KB
-constexpr int kFewSums = 16 * 1024;     // of which sums
-static_assert(few_pitch(131072) <= kFewLds - kFewSums, "LDS holds the longest row");
-constexpr int kFewUnitsOfGpu = 256;     // compute units: a workgroup on each
-
-bool few_fits(int64_t M, int64_t K) { return M <= kFewTokens && M * few_pitch((int)K) <= kFewLds; }
-
-// Each workgroup quantises the rows for itself, or copies the codes that a kernel ahead wrote.
-bool few_quantise(int64_t rows, int64_t K) { return rows * ((K + 511) / 512) <= kFewUnits; }
-
-// Column sets (of 4 tokens) a chunk has: all tokens where they are few, else a multiple of what an expert has on
-// average, as four sets take four times the products and code reads of one (an expert that has more is taken in two
-// chunks).
-int few_sets(int64_t M, int64_t topk, int64_t E) {
-    const int64_t most = E > 0 ? std::min(M, 4 * M * topk / E + 3) : M;
-    return most <= 4 ? 1 : (most <= 8 ? 2 : 4);
-}
-
 template <int T, int SRC, int NS>
 hipError_t run_front(const FewFrontParams& p, hipStream_t st) {
     const size_t lds = (size_t)p.M * few_pitch(p.K);
     const int64_t chunks = p.E > 0 ? std::min<int64_t>(p.E, p.M * p.topk) : 1, n = chunks * ((p.I + 1) / 2);
-    const unsigned grid = (unsigned)std::min<int64_t>(n, kFewUnitsOfGpu);
+    const unsigned grid = (unsigned)std::min<int64_t>(n, kFewGrid);
     auto k = SRC == kFewStaged || p.E <= 128 ? few_front_kernel<T, SRC, NS, 2>
                                              : few_front_kernel<T, SRC, NS, SRC == kFewStaged ? 2 : 16>;
     hipLaunchKernelGGL(k, dim3(grid), dim3(kFewThreads), lds, st, p);
@@ -228,13 +241,11 @@ hipError_t few_front(FewFrontParams& p, int8_t* xq, int64_t ldxq, float* xs, int
     return run_front<T, kFewStaged>(p, sets, st);
 }
 
-int few_down_rows(int P, int I) { return std::min(P, (kFewLds - kFewSums) / few_pitch(I)); }
-
 template <int T, int SRC>
 hipError_t run_down(FewDownParams& p, int sets, hipStream_t st) {
     const int P = p.M * p.topk, groups = (int)(p.H / 4), pitch = few_pitch(p.I);
-    p.rows = few_down_rows(P, p.I);
-    const int grid = std::min(groups, kFewUnitsOfGpu), most = (groups + grid - 1) / grid;
+    p.rows = (int)few_down_rows(P, p.I);
+    const int grid = std::min(groups, kFewGrid), most = (groups + grid - 1) / grid;
     p.block = std::max(1, std::min(most, kFewSums / (16 * P)));
     auto k = sets == 1 ? few_down_kernel<T, SRC, 1> : (sets == 2 ? few_down_kernel<T, SRC, 2> : few_down_kernel<T, SRC, 4>);
     hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(kFewThreads),
@@ -250,7 +261,7 @@ hipError_t few_moe(const I8MoeArgs& a, uint16_t* h, int8_t* xq, float* xs, int8_
     f.x = a.x; f.ldx = a.ldx; f.M = (int)a.M; f.K = (int)a.H; f.logits = a.logits; f.ldl = a.ldl; f.E = (int)a.E;
     f.topk = (int)a.topk; f.route = a.route; f.ids = a.ids; f.gw = a.gw; f.w = a.w13; f.ldw = a.ldw13; f.I = a.I;
     f.ws = a.s13; f.ws_step = 1; f.act = a.act; f.y = h; f.ldy = a.I;
-    const int sets = few_sets(a.M, a.topk, a.E), cap = std::min(4 * sets, few_down_rows((int)P, (int)a.I));
+    const int sets = few_sets(a.M, a.topk, a.E), cap = (int)few_chunk(a.M, a.topk, a.E, a.I);
     hipError_t e = few_front<T>(f, xq, a.H, xs, sets, cap, list, st);
     if (e != hipSuccess) return e;
     FewDownParams d{};
@@ -279,24 +290,30 @@ hipError_t moe(const I8MoeArgs& a, hipStream_t st) {
     uint16_t* h = (uint16_t*)(ws + r.h);
     int32_t *offs = (int32_t*)(ws + r.offs), *toffs = (int32_t*)(ws + r.toffs), *perm = (int32_t*)(ws + r.perm);
     if (few_fits(a.M, a.H)) return few_moe<T>(a, h, xq, xs, hq, hs, (FewList*)(ws + r.list), st);
-    hipError_t e = a.logits ? route(a, st) : hipSuccess;
+    const int bm = (int)i8_tile_rows(P, a.E);
+    const bool one = a.logits && a.M <= kI8PrepTokens;  // one launch routes, sorts and quantises
+    hipError_t e = a.logits && !one ? route(a, st) : hipSuccess;
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(i8_sort_kernel, dim3(1), dim3(1024), 0, st, a.ids, (int)P, (int)a.E, kI8Bm, offs, toffs, perm);
+    const I8PrepParams q{a.x, a.ldx, a.M, a.H, xq, xs, a.logits, a.ldl, (int)a.E, (int)a.topk, a.route, bm,
+                         a.ids, a.gw, offs, toffs, perm};
+    auto prep = !one ? i8_prep_kernel<T, 0> : (a.E <= 128 ? i8_prep_kernel<T, 2> : i8_prep_kernel<T, 16>);
+    hipLaunchKernelGGL(prep, dim3((unsigned)a.M + 1), dim3(1024), 0, st, q);
     e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    e = quantise(T, a.x, a.ldx, a.M, a.H, xq, a.H, xs, nullptr, 0, st);
     if (e != hipSuccess) return e;
     I8GemmParams g{};
     g.x = xq; g.ldx = a.H; g.xs = xs; g.offs = offs; g.toffs = toffs; g.perm = perm; g.div = (int)a.topk; g.E = (int)a.E;
     g.K = a.H; g.w = a.w13; g.ldw = a.ldw13; g.N = 2 * a.I; g.ws = a.s13; g.ws_step = 1; g.C = a.I; g.act = a.act;
     g.y = h; g.ldy = a.I;
-    e = run_gemm<T, kI8Gated, 128, kI8Bm, 2, 2>(g, most_tiles(P, a.E, kI8Bm), st);
+    const int64_t tiles = most_tiles(P, a.E, bm);
+    e = bm == 64 ? run_gemm<T, kI8Gated, 128, 64, 2, 2>(g, tiles, 0, a.I, st)
+                 : run_gemm<T, kI8Gated, 128, 128, 2, 4>(g, tiles, 0, a.I, st);
     if (e != hipSuccess) return e;
     e = quantise(T, h, a.I, P, a.I, hq, a.I, hs, a.ids, a.E, st);
     if (e != hipSuccess) return e;
     g.x = hq; g.ldx = a.I; g.xs = hs; g.div = 1; g.K = a.I; g.w = a.w2; g.ldw = a.ldw2; g.N = a.H; g.ws = a.s2;
     g.C = a.H; g.y = nullptr; g.part = part; g.ldy = a.H;
-    e = run_gemm<T, kI8Part, 128, kI8Bm, 2, 2>(g, most_tiles(P, a.E, kI8Bm), st);
+    e = bm == 64 ? run_gemm<T, kI8Part, 128, 64, 4, 2>(g, tiles, 0, a.H, st)
+                 : run_gemm<T, kI8Part, 128, 128, 2, 4>(g, tiles, 0, a.H, st);
     if (e != hipSuccess) return e;
     const int64_t n = a.M * (a.H / 4);
     hipLaunchKernelGGL(i8_combine_kernel<T>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, part, a.ids, a.gw, a.M,
@@ -318,7 +335,13 @@ hipError_t glu(const I8GluArgs& a, hipStream_t st) {
     g.x = a.xq; g.ldx = a.ldxq; g.xs = a.xs; g.R = a.M; g.E = 1; g.div = 1;
     g.K = a.K; g.w = a.w13; g.ldw = a.ldw; g.N = 2 * a.I; g.ws = a.s13; g.ws_step = a.ws_step; g.C = a.I; g.act = a.act;
     g.y = a.y; g.ldy = a.ldy;
-    return run_gemm<T, kI8Gated, 128, 64, 2, 2>(g, (a.M + 63) / 64, st);
+    if (i8_dense_rows(a.M) == 64) return run_gemm<T, kI8Gated, 128, 64, 2, 2>(g, 1, 0, a.I, st);
+    const int64_t large = i8_large_columns(a.M, a.I);
+    if (large > 0) {
+        const hipError_t l = run_gemm<T, kI8Gated, 256, 256, 4, 4>(g, (a.M + 255) / 256, 0, large, st);
+        if (l != hipSuccess || large == a.I) return l;
+    }
+    return run_gemm<T, kI8Gated, 128, 128, 2, 4>(g, (a.M + 127) / 128, large, a.I - large, st);
 }
 
 }  // namespace

@@ -22,12 +22,9 @@
 #include <type_traits>
 
 #include "i8ffn_device.hpp"
+#include "i8ffn_plan.hpp"
 
 namespace qlin {
-
-constexpr int kFewPairs = 256;   // 16 tokens, 16 slots
-constexpr int kFewThreads = 512, kFewWaves = kFewThreads / 64;  // one workgroup a compute unit
-constexpr int kFewTokens = 16;   // tokens of a chunk: four columns sets
 
 typedef int i32x4f_t __attribute__((ext_vector_type(4)));
 
@@ -144,19 +141,11 @@ __device__ __forceinline__ int blocks_sum(int v) {
     return (int)(a + b);
 }
 
-// Steps of 256 K that a wave's loads are ahead of its products.
-constexpr int kFewDepth = 4;
-
-// LDS pitch of a code row: whole turns of the loads' ring, and the four tokens of a column set 64 bytes (16 banks) apart
-__host__ __device__ constexpr int few_pitch(int K) { return (K + 256 * kFewDepth - 1) / (256 * kFewDepth) * (256 * kFewDepth) + 64; }
-
 // Where the codes come from.
 enum FewSrc { kFewQuantise = 0, kFewStaged = 1 };
 
 // A workgroup quantises up to kFewUnits x 512 elements into its LDS: a unit is 512 elements of one row, one load a
 // lane.  The loads are issued by the constructor, long before their use.
-constexpr int kFewUnitsPerWave = 6, kFewUnits = kFewUnitsPerWave * kFewWaves;
-
 template <int T>
 struct FewQuantiser {
     u32x4_t v[kFewUnitsPerWave];

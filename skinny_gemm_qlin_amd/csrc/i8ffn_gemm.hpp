@@ -27,6 +27,7 @@ struct I8GemmParams {
     int64_t K; const int8_t* w; int64_t ldw; int64_t N;  // N weight rows a group (gated: 2 I)
     const float* ws; int ws_step;                   // [E][N]
     int64_t C;                                      // output columns: I or N
+    int64_t c_first, c_count;                       // of which this launch computes c_count from c_first
     int act; uint16_t* y; float* part; int64_t ldy;
 };
 
@@ -48,19 +49,19 @@ __device__ __forceinline__ void i8_stage_barrier() {
 constexpr int64_t kI8BandM = 8;  // row tiles per raster band
 
 template <int T, int EPI, int BN, int BM, int WGN, int WGM>
-__global__ __launch_bounds__(64 * WGM * WGN, 2) void i8_gemm_kernel(const I8GemmParams p) {
+__global__ __launch_bounds__(64 * WGM * WGN, WGM * WGN == 16 ? 4 : 2) void i8_gemm_kernel(const I8GemmParams p) {
     constexpr int NW = WGM * WGN;
     constexpr int TM = BM / WGM / 32, TN = BN / WGN / 32;  // 32 x 32 tiles per wave
     constexpr int BK = 128, XT = BM * BK, WT = BN * BK;
     constexpr int XI = BM / 8 / NW, WI = BN / 8 / NW;      // 1 KB loads per wave and step
     constexpr int CT = EPI == kI8Gated ? BN / 2 : BN;      // output columns a tile
-    static_assert(TM >= 1 && TN >= 1 && XI >= 1 && WI >= 1 && (EPI != kI8Gated || TN == 2), "tile");
+    static_assert(TM >= 1 && TN >= 1 && XI >= 1 && WI >= 1 && (EPI != kI8Gated || TN % 2 == 0), "tile");
     // an object of its own for each tile: a load into one need not be waited for before another is read
     __shared__ __align__(16) uint8_t x_even[XT], x_odd[XT], w_even[WT], w_odd[WT];
     __shared__ int32_t rows[BM];  // grouped: the tile's pairs
 
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-    const int64_t tiles_c = (p.C + CT - 1) / CT;
+    const int64_t tiles_c = (p.c_count + CT - 1) / CT;
     int64_t c0, m0, cnt;  // first column; first row and number of rows of the tile
     int e = 0;
     const int b = blockIdx.x;
@@ -78,7 +79,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, 2) void i8_gemm_kernel(const I8Gemm
         }
         e = lo;
         const int64_t mt = p.toffs[e + 1] - p.toffs[e], rr = t - p.toffs[e] * tiles_c;
-        c0 = rr / mt * CT;
+        c0 = p.c_first + rr / mt * CT;
         m0 = p.offs[e] + rr % mt * BM;
         cnt = p.offs[e + 1] - m0;
     } else {
@@ -87,7 +88,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, 2) void i8_gemm_kernel(const I8Gemm
         if (b / 8 >= per || t >= tiles) return;  // workgroup-uniform
         const int64_t bsz = kI8BandM * tiles_c, band = t / bsz, rr = t - band * bsz;
         const int64_t gm = tiles_m - band * kI8BandM < kI8BandM ? tiles_m - band * kI8BandM : kI8BandM;
-        c0 = rr / gm * CT;
+        c0 = p.c_first + rr / gm * CT;
         m0 = (band * kI8BandM + rr % gm) * BM;
         cnt = p.R - m0;
     }
@@ -196,10 +197,13 @@ __global__ __launch_bounds__(64 * WGM * WGN, 2) void i8_gemm_kernel(const I8Gemm
             const int64_t pair = p.offs ? rows[r] : m0 + r;
             const float xs = p.xs[p.offs ? pair / p.div : pair];
             if constexpr (EPI == kI8Gated) {
-                const int64_t c = c0 + wn * 32 + row;
-                if (c >= C) continue;
-                p.y[pair * p.ldy + c] = f32_to_h<T>(
-                    gated(acc[i][0][v], acc[i][1][v], xs, ws[c * p.ws_step], ws[(C + c) * p.ws_step], p.act));
+#pragma unroll
+                for (int j = 0; j < TN; j += 2) {
+                    const int64_t c = c0 + wn * (BN / WGN / 2) + j / 2 * 32 + row;
+                    if (c < C)
+                        p.y[pair * p.ldy + c] = f32_to_h<T>(gated(acc[i][j][v], acc[i][j + 1][v], xs, ws[c * p.ws_step],
+                                                                  ws[(C + c) * p.ws_step], p.act));
+                }
             } else {
 #pragma unroll
                 for (int j = 0; j < TN; ++j) {

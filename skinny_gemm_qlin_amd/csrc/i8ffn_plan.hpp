@@ -1,0 +1,66 @@
+// i8ffn_plan.hpp -- which kernel the INT8 feed-forward operators take, by sizes
+// alone: plain C++, so that a host test can ask too.
+#pragma once
+#include <stddef.h>
+#include <stdint.h>
+
+namespace qlin {
+
+// ---------------------------------------------------------------- up to 16 tokens: i8ffn_few.hpp
+constexpr int kFewPairs = 256;   // 16 tokens, 16 slots
+constexpr int kFewThreads = 512, kFewWaves = kFewThreads / 64;  // one workgroup a compute unit: 16 waves, or two workgroups, are slower
+constexpr int kFewTokens = 16;   // tokens of a chunk at most: four column sets
+constexpr int kFewDepth = 4;     // steps of 256 K that a wave's loads are ahead of its products (a turn)
+constexpr int kFewUnitsPerWave = 6, kFewUnits = kFewUnitsPerWave * kFewWaves;  // x 512 elements that a workgroup quantises
+constexpr int kFewLds = 146 * 1024;  // dynamic LDS next to the lists, of 160 KB
+constexpr int kFewSums = 16 * 1024;  // of which the down projection's sums
+constexpr int kFewGrid = 256;        // compute units
+
+// LDS pitch of a code row: whole turns, and the four tokens of a column set 64 bytes (16 banks) apart
+constexpr int few_pitch(int64_t K) {
+    return (int)((K + 256 * kFewDepth - 1) / (256 * kFewDepth) * (256 * kFewDepth)) + 64;
+}
+static_assert(few_pitch(131072) <= kFewLds - kFewSums, "LDS holds the longest row");
+
+// All tokens' codes are in LDS at once.  (9 to 16 rows longer than that go to the GEMM.)
+constexpr bool few_fits(int64_t M, int64_t K) { return M <= kFewTokens && M * few_pitch(K) <= kFewLds; }
+
+// Each workgroup quantises the rows for itself, or copies the codes that a kernel ahead wrote.
+constexpr bool few_quantise(int64_t rows, int64_t K) { return rows * ((K + 511) / 512) <= kFewUnits; }
+
+// Column sets (of 4 tokens) a chunk has: all tokens where they are few, else a multiple of what an expert has on
+// average, as four sets take four times the products and code reads of one (an expert that has more is taken in two
+// chunks).  E = 0: dense.
+constexpr int few_sets(int64_t M, int64_t topk, int64_t E) {
+    const int64_t often = E > 0 ? 4 * M * topk / E + 3 : M, most = often < M ? often : M;
+    return most <= 4 ? 1 : (most <= 8 ? 2 : 4);
+}
+
+// Pairs' code rows that LDS holds in the down projection, and the pairs of a chunk.
+constexpr int64_t few_down_rows(int64_t P, int64_t I) {
+    const int64_t n = (kFewLds - kFewSums) / few_pitch(I);
+    return P < n ? P : n;
+}
+constexpr int64_t few_chunk(int64_t M, int64_t topk, int64_t E, int64_t I) {
+    const int64_t n = few_down_rows(M * topk, I), s = 4 * few_sets(M, topk, E);
+    return s < n ? s : n;
+}
+
+// ---------------------------------------------------------------- more: i8ffn_gemm.hpp
+// Code rows of a tile.  Dense: 64 up to 64 tokens (128 tokens of 2 x 14336 x 4096: 45 us with either, 256: 83 and 52).
+// Experts: by what they have on average (64 experts, 7168 x 2048, front and down: 28 pairs each 345 + 216 us with
+// 64 rows, 372 + 258 with 128; 94 pairs each 509 + 349 and 409 + 303).
+constexpr int i8_tile_rows(int64_t P, int64_t E) { return P <= 56 * E ? 64 : 128; }
+constexpr int i8_dense_rows(int64_t M) { return M <= 64 ? 64 : 128; }
+
+// Output columns of a dense front that 256 x 256 tiles (128 columns) compute in whole rounds of 256.
+constexpr int64_t i8_large_columns(int64_t M, int64_t I) {
+    if (M < 1024) return 0;
+    const int64_t mt = (M + 255) / 256, all = mt * (I / 128), rounds = all / 256;
+    return rounds * 256 / mt * 128;
+}
+
+// Tokens up to which one workgroup routes all of them and sorts the pairs, next to the ones that quantise them.
+constexpr int64_t kI8PrepTokens = 64;
+
+}  // namespace qlin
