@@ -24,12 +24,13 @@ LIB = os.path.join(PKG, "libqlin.so")
 
 SOURCES = ["gemv.hip", "ks_i8.hip", "ks_f8.hip", "ks_w8a8_e4m3.hip", "ks_w8a8_e5m2.hip", "qlin_api.hip",
            "act_quant.hip", "qlin_w4_api.hip", "w4_gemm.hip",
-           "w4_few_bf16.hip", "w4_few_fp16.hip", "w4_mid.hip", "qlin_i8ffn_api.hip", "i8ffn.hip", "gemm.hip", "moe.hip", "moe_prefill.hip", "routing.hip"]
+           "w4_few_bf16.hip", "w4_few_fp16.hip", "w4_mid.hip", "i8ffn_few_bf16.hip", "i8ffn_few_fp16.hip", "i8ffn.hip",
+           "qlin_i8ffn_api.hip", "gemm.hip", "moe.hip", "moe_prefill.hip", "routing.hip"]
 HEADERS = ["qlin_device.hpp", "qlin_launch.hpp", "gemv_kernels.hpp", "mfma_kernels.hpp", "ks_kernels.hpp",
            "ks_launch.hpp", "gemm_kernels.hpp", "w4_device.hpp", "w4_launch.hpp", "w4_gemm.hpp",
            "w4_mid.hpp", "w4_mid_launch.hpp", "w4_bwd.hpp", "w4_few.hpp", "w4_few_launch.hpp", "w4_plan.hpp",
            "i8ffn_launch.hpp", "i8ffn_device.hpp", "i8ffn_gemm.hpp", "i8ffn_few.hpp",
-           "i8ffn_plan.hpp"]
+           "i8ffn_few_impl.hpp", "i8ffn_few_launch.hpp", "i8ffn_plan.hpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

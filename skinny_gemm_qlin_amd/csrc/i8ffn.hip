@@ -1,11 +1,10 @@
 // i8ffn.hip -- the INT8 feed-forward operators: row quantiser, routing, pair
 // sort and combine kernels, and the launchers of the gated front
 // (qlin_glu_i8) and the routed expert layer (qlin_moe_ffn_i8).
-#include <algorithm>
-
-#include "i8ffn_few.hpp"
+#include "i8ffn_few_launch.hpp"
 #include "i8ffn_gemm.hpp"
 #include "i8ffn_launch.hpp"
+#include "i8ffn_plan.hpp"
 
 namespace qlin {
 
@@ -190,94 +189,9 @@ MoeRegions regions(int64_t M, int64_t H, int64_t I, int64_t topk, int64_t E) {
     r.offs = take((E + 1) * 4);
     r.toffs = take((E + 1) * 4);
     r.perm = take(P * 4);
-    r.list = take(sizeof(FewList));
+    r.list = take((int64_t)few_list_bytes());
     r.total = at;
     return r;
-}
-
-// ---- up to 16 tokens
-template <int T, int SRC, int NS>
-hipError_t run_front(const FewFrontParams& p, hipStream_t st) {
-    const size_t lds = (size_t)p.M * few_pitch(p.K);
-    const int64_t chunks = p.E > 0 ? std::min<int64_t>(p.E, p.M * p.topk) : 1, n = chunks * ((p.I + 1) / 2);
-    const unsigned grid = (unsigned)std::min<int64_t>(n, kFewGrid);
-    auto k = SRC == kFewStaged || p.E <= 128 ? few_front_kernel<T, SRC, NS, 2>
-                                             : few_front_kernel<T, SRC, NS, SRC == kFewStaged ? 2 : 16>;
-    hipLaunchKernelGGL(k, dim3(grid), dim3(kFewThreads), lds, st, p);
-    return hipGetLastError();
-}
-
-template <int T, int SRC>
-hipError_t run_front(const FewFrontParams& p, int sets, hipStream_t st) {
-    if (sets == 1) return run_front<T, SRC, 1>(p, st);
-    return sets == 2 ? run_front<T, SRC, 2>(p, st) : run_front<T, SRC, 4>(p, st);
-}
-
-template <int T>
-hipError_t run_prep(const FewPrepParams& p, hipStream_t st) {
-    auto k = p.E <= 128 ? few_prep_kernel<T, 2> : few_prep_kernel<T, 16>;
-    hipLaunchKernelGGL(k, dim3((unsigned)(p.rows + (p.list ? 1 : 0))), dim3(kFewThreads), 0, st, p);
-    return hipGetLastError();
-}
-
-template <int T>
-hipError_t few_front(FewFrontParams& p, int8_t* xq, int64_t ldxq, float* xs, int sets, int cap, FewList* list,
-                     hipStream_t st) {
-    p.ldxq = ldxq;
-    if (few_quantise(p.M, p.K)) {
-        p.xq_out = p.E > 0 ? nullptr : xq;
-        p.xs_out = xs;
-        return run_front<T, kFewQuantise>(p, sets, st);
-    }
-    FewPrepParams q{};
-    q.x = p.x; q.ldx = p.ldx; q.rows = p.M; q.K = p.K; q.xq = xq; q.ldxq = ldxq; q.xs = xs; q.logits = p.logits;
-    q.ldl = p.ldl; q.M = p.M; q.E = p.E; q.topk = p.topk; q.route = p.route; q.cap = cap; q.ids = p.ids; q.gw = p.gw;
-    q.list = list;
-    const hipError_t e = run_prep<T>(q, st);
-    if (e != hipSuccess) return e;
-    p.xq = xq;
-    p.xs = xs;
-    p.list = list;
-    return run_front<T, kFewStaged>(p, sets, st);
-}
-
-template <int T, int SRC>
-hipError_t run_down(FewDownParams& p, int sets, hipStream_t st) {
-    const int P = p.M * p.topk, groups = (int)(p.H / 4), pitch = few_pitch(p.I);
-    p.rows = (int)few_down_rows(P, p.I);
-    const int grid = std::min(groups, kFewGrid), most = (groups + grid - 1) / grid;
-    p.block = std::max(1, std::min(most, kFewSums / (16 * P)));
-    auto k = sets == 1 ? few_down_kernel<T, SRC, 1> : (sets == 2 ? few_down_kernel<T, SRC, 2> : few_down_kernel<T, SRC, 4>);
-    hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(kFewThreads),
-                       (size_t)p.block * P * 16 + (size_t)p.rows * pitch, st, p);
-    return hipGetLastError();
-}
-
-template <int T>
-hipError_t few_moe(const I8MoeArgs& a, uint16_t* h, int8_t* xq, float* xs, int8_t* hq, float* hs, FewList* list,
-                   hipStream_t st) {
-    const int64_t P = a.M * a.topk;
-    FewFrontParams f{};
-    f.x = a.x; f.ldx = a.ldx; f.M = (int)a.M; f.K = (int)a.H; f.logits = a.logits; f.ldl = a.ldl; f.E = (int)a.E;
-    f.topk = (int)a.topk; f.route = a.route; f.ids = a.ids; f.gw = a.gw; f.w = a.w13; f.ldw = a.ldw13; f.I = a.I;
-    f.ws = a.s13; f.ws_step = 1; f.act = a.act; f.y = h; f.ldy = a.I;
-    const int sets = few_sets(a.M, a.topk, a.E), cap = (int)few_chunk(a.M, a.topk, a.E, a.I);
-    hipError_t e = few_front<T>(f, xq, a.H, xs, sets, cap, list, st);
-    if (e != hipSuccess) return e;
-    FewDownParams d{};
-    d.h = h; d.M = (int)a.M; d.I = (int)a.I; d.ids = a.ids; d.gw = a.gw; d.E = (int)a.E;
-    d.topk = (int)a.topk; d.w = a.w2; d.ldw = a.ldw2; d.H = a.H; d.ws = a.s2; d.y = a.y; d.ldy = a.ldy;
-    if (few_quantise(P, a.I)) return run_down<T, kFewQuantise>(d, sets, st);
-    FewPrepParams q{};
-    q.x = h; q.ldx = a.I; q.rows = (int)P; q.K = (int)a.I; q.xq = hq; q.ldxq = a.I; q.xs = hs; q.pairs = true; q.M = (int)a.M;
-    q.E = (int)a.E; q.topk = (int)a.topk; q.cap = cap; q.ids = a.ids; q.gw = a.gw;
-    q.list = few_quantise(a.M, a.H) ? list : nullptr;  // the front made its list for itself
-    e = run_prep<T>(q, st);
-    if (e != hipSuccess) return e;
-    d.hq = hq;
-    d.hs = hs;
-    d.list = list;
-    return run_down<T, kFewStaged>(d, sets, st);
 }
 
 template <int T>
@@ -289,7 +203,10 @@ hipError_t moe(const I8MoeArgs& a, hipStream_t st) {
     float *xs = (float*)(ws + r.xs), *hs = (float*)(ws + r.hs), *part = (float*)(ws + r.part);
     uint16_t* h = (uint16_t*)(ws + r.h);
     int32_t *offs = (int32_t*)(ws + r.offs), *toffs = (int32_t*)(ws + r.toffs), *perm = (int32_t*)(ws + r.perm);
-    if (few_fits(a.M, a.H)) return few_moe<T>(a, h, xq, xs, hq, hs, (FewList*)(ws + r.list), st);
+    if (few_fits(a.M, a.H)) {
+        const I8FewRegions f{xq, xs, h, hq, hs, ws + r.list};
+        return T == kFp16 ? few_moe_fp16(a, f, st) : few_moe_bf16(a, f, st);
+    }
     const int bm = (int)i8_tile_rows(P, a.E);
     const bool one = a.logits && a.M <= kI8PrepTokens;  // one launch routes, sorts and quantises
     hipError_t e = a.logits && !one ? route(a, st) : hipSuccess;
@@ -323,12 +240,7 @@ hipError_t moe(const I8MoeArgs& a, hipStream_t st) {
 
 template <int T>
 hipError_t glu(const I8GluArgs& a, hipStream_t st) {
-    if (few_fits(a.M, a.K)) {
-        FewFrontParams f{};
-        f.x = a.x; f.ldx = a.ldx; f.M = (int)a.M; f.K = (int)a.K; f.w = a.w13; f.ldw = a.ldw; f.I = a.I; f.ws = a.s13;
-        f.ws_step = a.ws_step; f.act = a.act; f.y = a.y; f.ldy = a.ldy;
-        return few_front<T>(f, a.xq, a.ldxq, a.xs, few_sets(a.M, 0, 0), 0, nullptr, st);
-    }
+    if (few_fits(a.M, a.K)) return T == kFp16 ? few_glu_fp16(a, st) : few_glu_bf16(a, st);
     const hipError_t e = quantise(T, a.x, a.ldx, a.M, a.K, a.xq, a.ldxq, a.xs, nullptr, 0, st);
     if (e != hipSuccess) return e;
     I8GemmParams g{};

@@ -41,28 +41,57 @@ __device__ __forceinline__ uint32_t wave_mag(uint32_t m) {
     return lo > hi ? lo : hi;
 }
 
-// s and fl64(1 / s) (0 where the codes are 0) of a row whose largest magnitude has the bits `mag`
+// The scale of a row whose largest magnitude has the bits `mag`, and what its codes are made with.
+//
+// The quotient.  From 2^-100 up: t = x * r with r = fl(1 / s), then one step t + (x - t s) r in fused operations,
+// which gives the correctly rounded quotient (the remainder is exact; every mantissa of x against every scale that an
+// absolute maximum of the type can give is checked in the CPU tests).  No quotient rounds to more than 127 there.
+// Below, where the remainder may be subnormal: through 64 bits, as div_bf16.
+struct RowScale {
+    float s, r;
+    double rd;
+    bool fine;  // the first way
+};
+
 template <int T>
-__device__ __forceinline__ float row_scale(uint32_t mag, double& r) {
+__device__ __forceinline__ RowScale row_scale(uint32_t mag) {
     const uint32_t inf = T == kBf16 ? 0x7F80u : 0x7C00u;
-    const float s = mag >= inf ? __uint_as_float(0x7FC00000u) : h_to_f32<T>(mag) / 127.0f;
-    r = mag == 0 || mag >= inf ? 0.0 : 1.0 / (double)s;
-    return s;
+    RowScale o;
+    o.s = mag >= inf ? __uint_as_float(0x7FC00000u) : h_to_f32<T>(mag) / 127.0f;
+    o.fine = o.s >= 0x1p-100f;
+    o.r = o.fine ? 1.0f / o.s : 0.0f;
+    o.rd = 0.0;
+    if (!o.fine && mag != 0 && mag < inf) o.rd = 1.0 / (double)o.s;  // else the codes are 0
+    return o;
 }
 
-// 8 values -> 8 codes; r = 0 gives codes 0 (a non-finite value times 0 is NaN, which v_cvt_i32_f32 turns into 0)
+__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {  // low bytes
+    const uint32_t lo = __builtin_amdgcn_perm((uint32_t)b, (uint32_t)a, 0x0C0C0400u);
+    const uint32_t hi = __builtin_amdgcn_perm((uint32_t)d, (uint32_t)c, 0x04000C0Cu);
+    return lo | hi;
+}
+
+// 8 values -> 8 codes
 template <int T>
-__device__ __forceinline__ uint2 codes8(const u32x4_t& v, double r) {
+__device__ __forceinline__ uint2 codes8(const u32x4_t& v, const RowScale& o) {
     const uint32_t d[4] = {v.x, v.y, v.z, v.w};
-    uint32_t packed[2] = {0u, 0u};
+    int q[8];
+    if (o.fine) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t h = (e & 1) ? (d[e >> 1] >> 16) : (d[e >> 1] & 0xFFFFu);
-        float t = rintf(div_bf16(h_to_f32<T>(h), r));
-        t = fminf(fmaxf(t, -127.0f), 127.0f);
-        packed[e >> 2] |= ((uint32_t)(r == 0.0 ? 0 : (int)t) & 0xFFu) << (8 * (e & 3));
+        for (int e = 0; e < 8; ++e) {
+            const float x = h_to_f32<T>((e & 1) ? (d[e >> 1] >> 16) : (d[e >> 1] & 0xFFFFu));
+            const float t = x * o.r;
+            q[e] = (int)rintf(fmaf(fmaf(-t, o.s, x), o.r, t));
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float x = h_to_f32<T>((e & 1) ? (d[e >> 1] >> 16) : (d[e >> 1] & 0xFFFFu));
+            const float t = fminf(fmaxf(rintf(div_bf16(x, o.rd)), -127.0f), 127.0f);
+            q[e] = o.rd == 0.0 ? 0 : (int)t;
+        }
     }
-    return make_uint2(packed[0], packed[1]);
+    return make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
 }
 
 // A workgroup of NT threads quantises a row: largest magnitude, then codes.
@@ -87,15 +116,14 @@ __device__ __forceinline__ void quantise_row_wg(const uint16_t* row, int64_t K, 
     uint32_t mag = part[0];
 #pragma unroll
     for (int q = 1; q < W; ++q) mag = part[q] > mag ? part[q] : mag;
-    double r;
-    const float s = row_scale<T>(mag, r);
-    if (tid == 0) *scale = s;
+    const RowScale o = row_scale<T>(mag);
+    if (tid == 0) *scale = o.s;
 #pragma unroll
     for (int c = 0; c < CACHED; ++c) {
         const int64_t i = tid + c * NT;
-        if (i < nvec) *(uint2*)(out + i * 8) = codes8<T>(cache[c], r);
+        if (i < nvec) *(uint2*)(out + i * 8) = codes8<T>(cache[c], o);
     }
-    for (int64_t i = tid + CACHED * NT; i < nvec; i += NT) *(uint2*)(out + i * 8) = codes8<T>(ld16(row + i * 8), r);
+    for (int64_t i = tid + CACHED * NT; i < nvec; i += NT) *(uint2*)(out + i * 8) = codes8<T>(ld16(row + i * 8), o);
 }
 
 // act(g) u of the int32 sums of a gate and an up row

@@ -37,9 +37,9 @@ __device__ __forceinline__ int few_div(int x, int d, float r) {
 
 // Pairs by expert, in chunks of up to `cap` pairs of one expert (at most kFewTokens).
 struct FewList {
-    int chunks, pad[3];
-    int expert[kFewPairs], first[kFewPairs], count[kFewPairs];  // of each chunk
-    int pair[kFewPairs], token[kFewPairs];                      // pairs in expert order, pair order inside; their tokens
+    int chunks, pairs, pad[2];
+    i32x4f_t chunk[kFewPairs];              // expert, first pair, number of pairs
+    int pair[kFewPairs], token[kFewPairs];  // pairs in expert order, pair order inside; their tokens
 };
 
 struct FewListTemp {
@@ -95,11 +95,11 @@ __device__ __forceinline__ void few_list(FewList& l, FewListTemp& t, int npairs,
     if (head) {
         int c = __popcll(hm & ((1ull << lane) - 1ull));
         for (int q = 0; q < wv; ++q) c += t.heads[q];
-        l.expert[c] = t.sid[l.pair[tid]];
-        l.first[c] = tid;
-        l.count[c] = cnt - b4 < cap ? cnt - b4 : cap;
+        l.chunk[c] = i32x4f_t{t.sid[l.pair[tid]], tid, cnt - b4 < cap ? cnt - b4 : cap, 0};
     }
     if (tid == 0) l.chunks = t.heads[0] + t.heads[1] + t.heads[2] + t.heads[3];
+    if (m >= 0 && (tid + 1 == kFewPairs || t.meta[tid + 1] < 0)) l.pairs = tid + 1;
+    if (tid == 0 && m < 0) l.pairs = 0;
     w4_lds_barrier();
 }
 
@@ -130,16 +130,20 @@ __device__ __forceinline__ void few_route(const float* logits, int64_t ldl, int 
     }
 }
 
-// sum over the 16 blocks: lanes of equal lane % 4; every lane gets it
-__device__ __forceinline__ int blocks_sum(int v) {
-    v += dpp_mov<0x128>(v);
-    v += dpp_mov<0x124>(v);
-    uint32_t a = (uint32_t)v, b = (uint32_t)v;
+// Adds a wave's four accumulators over the 16 blocks: lane l gets the sum of row few_row(l), column l % 4.  Lanes 32
+// and 16 apart first, where a swap and an addition put two accumulators' halves side by side.
+__device__ __forceinline__ int blocks_sum(const i32x4f_t& acc) {
+    uint32_t a = (uint32_t)acc[0], b = (uint32_t)acc[1], c = (uint32_t)acc[2], d = (uint32_t)acc[3];
     swap32(a, b);
-    a = b = a + b;
-    swap16(a, b);
-    return (int)(a + b);
+    swap32(c, d);
+    a += b;  // row 0 in lanes ..31, row 1 above
+    c += d;  // row 2, row 3
+    swap16(a, c);
+    int v = (int)(a + c);  // rows 0, 2, 1, 3 in lanes 0.., 16.., 32.., 48..
+    v += dpp_mov<0x128>(v);
+    return v + dpp_mov<0x124>(v);
 }
+__device__ __forceinline__ int few_row(int lane) { return ((lane >> 4) & 1) * 2 + (lane >> 5); }
 
 // Where the codes come from.
 enum FewSrc { kFewQuantise = 0, kFewStaged = 1 };
@@ -184,7 +188,7 @@ struct FewQuantiser {
     // after a barrier; zeros from K to the pitch
     __device__ void codes(const uint32_t* mag, int8_t* out, float* scale, int pitch) const {
         int last = -1;
-        double r = 0.0;
+        RowScale o{};
 #pragma unroll
         for (int i = 0; i < kFewUnitsPerWave; ++i) {
             if (i * kFewWaves + wv >= units) break;  // uniform
@@ -192,11 +196,11 @@ struct FewQuantiser {
             where(i, m, seg);
             const int k = seg * 512 + lane * 8;
             if (m != last) {  // uniform
-                const float s = row_scale<T>(mag[m], r);
-                if (lane == 0) scale[m] = s;  // every wave of the row writes the same
+                o = row_scale<T>((uint32_t)__builtin_amdgcn_readfirstlane((int)mag[m]));
+                if (lane == 0) scale[m] = o.s;  // every wave of the row writes the same
                 last = m;
             }
-            if (k < pitch) *(uint2*)(out + m * pitch + k) = codes8<T>(v[i], r);  // past K: zeros give zeros
+            if (k < pitch) *(uint2*)(out + m * pitch + k) = codes8<T>(v[i], o);  // past K: zeros give zeros
         }
         const int done = segs * 512;  // the rest of the ring's turn
         for (int m = wv; m < rows; m += kFewWaves)
@@ -206,15 +210,17 @@ struct FewQuantiser {
 
 __device__ const u32x4_t kFewZero16 = {0u, 0u, 0u, 0u};
 
-// Copies code rows (row r is xq's row of[r], or r) to LDS, 1 KB a load instruction, zeros past K; the caller waits.
+// Copies code rows (row r is xq's row of[r], or r) to LDS, 1 KB a load instruction, zeros from K to the end of the last
+// turn; the caller waits.
 __device__ __forceinline__ void stage_codes(const int8_t* xq, int64_t ldxq, const int* of, int rows, int K, int pitch,
                                             int8_t* out) {
-    const int lane = threadIdx.x & 63;
+    const int lane = threadIdx.x & 63, span = pitch - 64;
     for (int r = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); r < rows; r += kFewWaves) {
         const int8_t* src = xq + (of ? __builtin_amdgcn_readfirstlane(of[r]) : r) * ldxq + lane * 16;
-        for (int k = 0; k < K; k += 1024)
-            __builtin_amdgcn_global_load_lds(k + lane * 16 < K ? (const void*)(src + k) : (const void*)&kFewZero16,
-                                             (lds_void_t*)(out + r * pitch + k), 16, 0, 0);
+        for (int k = 0; k < span; k += 1024)
+            if (k + lane * 16 < span)  // lanes past it write nothing
+                __builtin_amdgcn_global_load_lds(k + lane * 16 < K ? (const void*)(src + k) : (const void*)&kFewZero16,
+                                                 (lds_void_t*)(out + r * pitch + k), 16, 0, 0);
     }
 }
 
@@ -228,10 +234,11 @@ __device__ __forceinline__ void few_staged_barrier() {
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
-// What a wave has requested: kFewDepth steps (a turn) of its item, and the item's channel scales.  The ring is always
-// full: behind an item's last turn follows the next item's first.
+// What a wave has requested: D steps (a turn) of its item, and the item's channel scales.  The ring is always full:
+// behind an item's last turn follows the next item's first.
+template <int D>
 struct FewRing {
-    u32x4_t w[kFewDepth];
+    u32x4_t w[D];
     f32x2v_t sc;
     const int8_t* wp;
 
@@ -239,19 +246,20 @@ struct FewRing {
         const int at = ((threadIdx.x & 63) >> 2) * 16;
         wp = row;
 #pragma unroll
-        for (int u = 0; u < kFewDepth; ++u) {
-            const int k = (turn * kFewDepth + u) * 256 + at;
+        for (int u = 0; u < D; ++u) {
+            const int k = (turn * D + u) * 256 + at;
             w[u] = ld_stream(wp + (k < K ? k : 0));  // past K: any of the row, against zero codes
         }
     }
 };
 
-// Turns [t, end) of an item, at least one: its sums with NS x 4 columns, cb[n] the code row (LDS, zeros past K) of this
-// lane's token of set n.
-template <int NS>
-__device__ __forceinline__ void few_item(FewRing& ring, const int8_t* next, int t, int end, int K,
-                                         const int8_t* const (&cb)[NS], i32x4f_t (&acc)[NS]) {
-    constexpr int D = kFewDepth;
+// Turns [t, end) of an item, at least one: this lane's sums (blocks_sum) with NS x 4 columns, cb[n] where in few_lds the code
+// row of its token of set n lies (zeros past K).
+template <int NS, int D>
+__device__ __forceinline__ void few_item(FewRing<D>& ring, const int8_t* next, int t, int end, int K,
+                                         const int (&cb)[NS], int (&sum)[NS]) {
+    extern __shared__ __align__(16) uint8_t few_lds[];
+    i32x4f_t acc[NS];
     const int at = ((threadIdx.x & 63) >> 2) * 16;
 #pragma unroll
     for (int n = 0; n < NS; ++n) acc[n] = i32x4f_t{0, 0, 0, 0};
@@ -263,12 +271,12 @@ __device__ __forceinline__ void few_item(FewRing& ring, const int8_t* next, int 
         }
         u32x4_t x[2][NS];  // codes of this step and the next
 #pragma unroll
-        for (int n = 0; n < NS; ++n) x[0][n] = *(const u32x4_t*)(cb[n] + t * D * 256 + at);
+        for (int n = 0; n < NS; ++n) x[0][n] = *(const u32x4_t*)(few_lds + cb[n] + t * D * 256 + at);
 #pragma unroll
         for (int u = 0; u < D; ++u) {
             if (u + 1 < D) {
 #pragma unroll
-                for (int n = 0; n < NS; ++n) x[(u + 1) & 1][n] = *(const u32x4_t*)(cb[n] + (t * D + u + 1) * 256 + at);
+                for (int n = 0; n < NS; ++n) x[(u + 1) & 1][n] = *(const u32x4_t*)(few_lds + cb[n] + (t * D + u + 1) * 256 + at);
             }
 #pragma unroll
             for (int d = 0; d < 4; ++d)
@@ -281,9 +289,7 @@ __device__ __forceinline__ void few_item(FewRing& ring, const int8_t* next, int 
         }
     } while (++t < end);
 #pragma unroll
-    for (int n = 0; n < NS; ++n)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[n][r] = blocks_sum(acc[n][r]);
+    for (int n = 0; n < NS; ++n) sum[n] = blocks_sum(acc[n]);
 }
 
 // first of share `me`, where every share has q and the first r one more
@@ -292,22 +298,23 @@ __device__ __forceinline__ int few_first(int q, int r, int me) { return me * q +
 // Sums of the items that more than one wave had turns of: [wave that had its first turn][token][row], zeroed ahead.
 typedef int FewSlots[kFewWaves][kFewTokens][4];
 
-// A workgroup's items, chunks x `per` of them, are dealt to its waves by turns of 1024 K: every wave has as many as
+// A workgroup's items, chunks x `per` of them, are dealt to its waves by turns of D x 256 K: every wave has as many as
 // any other, to one.  An item that lies on the border of two waves is joined in LDS, in whole numbers.
-//   enter(c): the chunk's weights; row(i), scales(i): the row that this lane loads of item i of the chunk entered
-//   last, and its channel scales; tokens(c, cb): looks up chunk c's tokens;
-//   done(i, acc, sc).
-template <int NS>
+//   enter(c): the chunk's weights, and its FewChunk; row(i), scales(i): the row that this lane loads of item i of the
+//   chunk entered last, and the channel scales that it needs; tokens(chunk, cb): looks up the tokens of a chunk;
+//   done(i, sum, sc).
+template <int NS, int D>
 struct FewWork {
     int per, turns, q, r;      // items a chunk, turns an item; turns a wave, and how many waves have one more
     int c, i, t, left;         // chunk, item in it, turn of it; turns that are left
+    i32x4f_t chunk;            // the chunk entered last
     int open_c, open_i;        // an item whose first turn was this wave's and whose last was not (open_c < 0: none)
 
     // items [first, first + items) of all
     template <class Enter, class Row, class Scales>
-    __device__ void prime(FewRing& ring, int first, int items, int wave, int K, const Enter& enter, const Row& row,
+    __device__ void prime(FewRing<D>& ring, int first, int items, int wave, int K, const Enter& enter, const Row& row,
                           const Scales& scales) {
-        turns = (K + 256 * kFewDepth - 1) / (256 * kFewDepth);
+        turns = (K + 256 * D - 1) / (256 * D);
         q = items * turns / kFewWaves;
         r = items * turns % kFewWaves;
         const int at = few_first(q, r, wave);
@@ -321,32 +328,32 @@ struct FewWork {
         left = __builtin_amdgcn_readfirstlane(left);
         open_c = -1;
         open_i = 0;
-        enter(c);
+        chunk = enter(c);
         ring.sc = scales(i);
         ring.prime(row(i), t, K);
     }
     template <class Enter, class Row, class Scales, class Tokens, class Done>
-    __device__ void run(FewRing& ring, int wave, int K, FewSlots& slots, const Enter& enter, const Row& row,
+    __device__ void run(FewRing<D>& ring, int wave, int K, FewSlots& slots, const Enter& enter, const Row& row,
                         const Scales& scales, const Tokens& tokens, const Done& done) {
-        const int8_t* cb[NS];
+        int cb[NS];
         const int lane = threadIdx.x & 63;
         int at = -1;
         while (left > 0) {
-            if (c != at) tokens(c, cb);
+            if (c != at) tokens(chunk, cb);
             at = c;
             const int here = i, t0 = t, end = turns - t < left ? turns : t + left;
             left -= end - t0;
             if (left > 0 && ++i == per) {  // past the end: this item's rows, again
                 i = 0;
-                enter(++c);
+                chunk = enter(++c);
             }
             t = 0;
             const int8_t* next = row(i);
             const f32x2v_t sc = scales(i);
-            i32x4f_t acc[NS];
-            few_item<NS>(ring, next, t0, end, K, cb, acc);
+            int sum[NS];
+            few_item<NS, D>(ring, next, t0, end, K, cb, sum);
             if (t0 == 0 && end == turns) {
-                done(here, acc, ring.sc);
+                done(here, sum, ring.sc);
             } else {
                 int home = wave;
                 if (t0 > 0) {  // the wave that has the item's first turn
@@ -357,11 +364,9 @@ struct FewWork {
                     open_c = at;
                     open_i = here;
                 }
-                if (lane < 4)
+                if ((lane & 15) < 4)
 #pragma unroll
-                    for (int s = 0; s < NS; ++s)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) atomicAdd(&slots[home][s * 4 + lane][k], acc[s][k]);
+                    for (int s = 0; s < NS; ++s) atomicAdd(&slots[home][s * 4 + (lane & 3)][few_row(lane)], sum[s]);
             }
             ring.sc = sc;
         }
@@ -371,13 +376,13 @@ struct FewWork {
     __device__ void close(int wave, FewSlots& slots, const Enter& enter, const Scales& scales, const Tokens& tokens,
                           const Done& done) {
         if (open_c < 0) return;
-        const int8_t* cb[NS];
-        i32x4f_t acc[NS];
-        tokens(open_c, cb);
-        enter(open_c);
+        int cb[NS];
+        const int lane = threadIdx.x & 63;
+        int sum[NS];
+        tokens(enter(open_c), cb);
 #pragma unroll
-        for (int s = 0; s < NS; ++s) acc[s] = *(const i32x4f_t*)slots[wave][s * 4 + (threadIdx.x & 3)];
-        done(open_i, acc, scales(open_i));
+        for (int s = 0; s < NS; ++s) sum[s] = slots[wave][s * 4 + (lane & 3)][few_row(lane)];
+        done(open_i, sum, scales(open_i));
     }
 };
 
@@ -439,7 +444,7 @@ __global__ __launch_bounds__(kFewThreads) void few_prep_kernel(const FewPrepPara
 
 // A workgroup owns a run of all chunks' items, two outputs each.
 // NR: only where the workgroup routes.
-template <int T, int SRC, int NS, int NR>
+template <int T, int SRC, int NS, int D, int NR>
 __global__ __launch_bounds__(kFewThreads, 2) void few_front_kernel(const FewFrontParams p) {
     extern __shared__ __align__(16) uint8_t few_lds[];  // codes [M][pitch]
     __shared__ __align__(16) FewList list;
@@ -448,7 +453,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_front_kernel(const FewFron
     __shared__ float scale[kFewTokens];
     __shared__ uint32_t mag[kFewTokens];
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int pitch = few_pitch(p.K);
+    const int pitch = few_pitch(p.K, D);
     const bool moe = p.E > 0;
     int8_t* codes = (int8_t*)few_lds;
     const int npairs = moe ? p.M * p.topk : p.M;
@@ -471,17 +476,19 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_front_kernel(const FewFron
         }
     }
     const int chunks = moe ? __builtin_amdgcn_readfirstlane(list.chunks) : 1;
-    FewWork<NS> work;
+    FewWork<NS, D> work;
     work.per = (int)((p.I + 1) / 2);  // items of a chunk
     int first_item, items;
     few_share(chunks * work.per, blockIdx.x, gridDim.x, first_item, items);
-    const int r4 = lane & 3, o = (lane >> 2) & 1, I = (int)p.I;
+    const int r4 = lane & 3, o = lane >> 5, I = (int)p.I;
     const int8_t* w = nullptr;
     const float* ws = nullptr;
     auto enter = [&](int c) {
-        const int e = moe && chunks > 0 ? __builtin_amdgcn_readfirstlane(list.expert[c]) : 0;
+        const i32x4f_t h = moe && chunks > 0 ? list.chunk[c] : i32x4f_t{0, 0, p.M, 0};
+        const int e = __builtin_amdgcn_readfirstlane(h[0]);
         w = p.w + (int64_t)e * 2 * p.I * p.ldw;
         ws = p.ws + (int64_t)e * 2 * p.I * p.ws_step;
+        return h;
     };
     auto row = [&](int it) {  // gate rows of outputs 2 it and 2 it + 1, then their up rows
         const int i = 2 * it + (r4 & 1), ic = i < I ? i : I - 1;
@@ -491,7 +498,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_front_kernel(const FewFron
         const int i = 2 * it + o, ic = i < I ? i : I - 1;
         return f32x2v_t{ws[ic * p.ws_step], ws[(I + ic) * p.ws_step]};
     };
-    FewRing ring;
+    FewRing<D> ring;
     work.prime(ring, items > 0 ? first_item : 0, items, wv, p.K, enter, row, scales);
     if constexpr (SRC == kFewQuantise) {
         quant.maxima(mag);
@@ -506,30 +513,30 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_front_kernel(const FewFron
             if (tid < p.M) p.xs_out[tid] = scale[tid];
         }
     } else {
-        few_staged_barrier<kFewDepth>();
+        few_staged_barrier<D>();
     }
     int row_of[NS], cnt = 0;
     float xs[NS];
-    auto tokens = [&](int c, const int8_t* (&cb)[NS]) {
-        cnt = moe ? __builtin_amdgcn_readfirstlane(list.count[c]) : p.M;
-        const int first = moe ? list.first[c] : 0;
+    auto tokens = [&](const i32x4f_t& chunk, int (&cb)[NS]) {
+        cnt = __builtin_amdgcn_readfirstlane(chunk[2]);
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-            const int j = s * 4 + r4 < cnt ? s * 4 + r4 : 0;
-            row_of[s] = moe ? list.pair[first + j] : j;
-            const int t = moe ? list.token[first + j] : j;
-            cb[s] = codes + t * pitch;
+            const int j = chunk[1] + (s * 4 + r4 < cnt ? s * 4 + r4 : 0);
+            row_of[s] = moe ? list.pair[j] : j;
+            const int t = moe ? list.token[j] : j;
+            cb[s] = t * pitch;  // the codes open few_lds
             xs[s] = scale[t];
         }
     };
-    auto done = [&](int it, i32x4f_t (&acc)[NS], const f32x2v_t& sc) {
+    auto done = [&](int it, int (&sum)[NS], const f32x2v_t& sc) {
         const int i = 2 * it + o;
-        if (lane >= 8 || i >= I) return;
 #pragma unroll
-        for (int s = 0; s < NS; ++s)
-            if (s * 4 + r4 < cnt)
-                p.y[row_of[s] * p.ldy + i] = f32_to_h<T>(gated(o ? acc[s][1] : acc[s][0], o ? acc[s][3] : acc[s][2], xs[s],
-                                                               sc[0], sc[1], p.act));
+        for (int s = 0; s < NS; ++s) {
+            uint32_t g = (uint32_t)sum[s], u = g;  // lanes 0..: gate of output 0, 16..: its up, 32.., 48..: of output 1
+            swap16(g, u);
+            const uint16_t v = f32_to_h<T>(gated((int)g, (int)u, xs[s], sc[0], sc[1], p.act));
+            if ((lane & 31) < 4 && i < I && s * 4 + r4 < cnt) p.y[row_of[s] * p.ldy + i] = v;
+        }
     };
     work.run(ring, wv, p.K, slots, enter, row, scales, tokens, done);
     w4_lds_barrier();
@@ -551,7 +558,7 @@ struct FewDownParams {
 // Workgroup b of G owns a run of the output's 4-row groups and takes all
 // experts through it, so the slots are joined in LDS, in slot order.  Where LDS
 // does not hold all pairs' codes, the chunks are taken in batches that it holds.
-template <int T, int SRC, int NS>
+template <int T, int SRC, int NS, int D>
 __global__ __launch_bounds__(kFewThreads, 2) void few_down_kernel(const FewDownParams p) {
     extern __shared__ __align__(16) uint8_t few_lds[];  // sums [block][P][4], then codes [rows][pitch]
     __shared__ __align__(16) FewList list;
@@ -560,9 +567,10 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_down_kernel(const FewDownP
     __shared__ float scale[kFewPairs];
     __shared__ uint32_t mag[kFewPairs];
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int npairs = p.M * p.topk, pitch = few_pitch(p.I);
+    const int npairs = p.M * p.topk, pitch = few_pitch(p.I, D);
     float* sums = (float*)few_lds;
-    int8_t* codes = (int8_t*)few_lds + (size_t)p.block * npairs * 16;
+    const int codes_at = p.block * npairs * 16;
+    int8_t* codes = (int8_t*)few_lds + codes_at;
     FewQuantiser<T> quant(p.h, p.I, SRC == kFewQuantise ? npairs : 0, p.I);
     few_clear(slots);
     few_sid(temp, npairs, p.ids, p.E);
@@ -574,9 +582,9 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_down_kernel(const FewDownP
         few_copy_list(list, p.list);
         w4_lds_barrier();
     }
-    const int chunks = __builtin_amdgcn_readfirstlane(list.chunks);
+    const int chunks = __builtin_amdgcn_readfirstlane(list.chunks), all_pairs = __builtin_amdgcn_readfirstlane(list.pairs);
     const int groups = (int)(p.H / 4);
-    FewWork<NS> work;
+    FewWork<NS, D> work;
     int g0, g1;
     few_share(groups, blockIdx.x, gridDim.x, g0, g1);
     g1 += g0;
@@ -588,21 +596,31 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_down_kernel(const FewDownP
     auto row = [&](int it) { return w + (uint64_t)(uint32_t)(4 * it) * (uint32_t)p.ldw; };
     auto scales = [&](int it) { return f32x2v_t{ws[4 * it], 0.f}; };
     auto enter = [&](int c) {
-        const int e = c1 > c0 ? __builtin_amdgcn_readfirstlane(list.expert[c0 + c]) : 0;
+        const i32x4f_t h = c1 > c0 ? list.chunk[c0 + c] : i32x4f_t{0, 0, 0, 0};
+        const int e = __builtin_amdgcn_readfirstlane(h[0]);
         w = p.w + ((int64_t)e * p.H + 4 * gb + r4) * p.ldw;
-        ws = p.ws + (int64_t)e * p.H + 4 * gb + ((lane >> 2) & 3);
+        ws = p.ws + (int64_t)e * p.H + 4 * gb + few_row(lane);
+        return h;
     };
-    FewRing ring;
+    FewRing<D> ring;
     auto open_batch = [&](bool restage) {  // from chunk c0: its codes are copied and its first weights requested
         nb = g1 - gb < p.block ? g1 - gb : p.block;
         c1 = c0;
-        base = c0 < chunks ? __builtin_amdgcn_readfirstlane(list.first[c0]) : 0;
-        pairs = 0;
-        while (c1 < chunks) {
-            const int n = __builtin_amdgcn_readfirstlane(list.count[c1]);
-            if (pairs + n > p.rows) break;
-            pairs += n;
-            ++c1;
+        base = c0 < chunks ? __builtin_amdgcn_readfirstlane(list.chunk[c0][1]) : 0;
+        pairs = all_pairs;
+        if (all_pairs <= p.rows) {
+            c1 = chunks;
+        } else {  // as many chunks as LDS holds the pairs of: 64 at a time
+            pairs = 0;
+            for (;;) {
+                const int c = c1 + lane;
+                const i32x4f_t h = list.chunk[c < kFewPairs ? c : 0];
+                const uint64_t in = __ballot(c < chunks && h[1] + h[2] - base <= p.rows);
+                const int n = in == ~0ull ? 64 : __builtin_ctzll(~in);  // places ascend: the first ones
+                c1 += n;
+                if (n < 64) break;
+            }
+            if (c1 > c0) pairs = __builtin_amdgcn_readfirstlane(list.chunk[c1 - 1][1] + list.chunk[c1 - 1][2]) - base;
         }
         work.per = nb;
         if (SRC == kFewStaged && restage) stage_codes(p.hq, p.I, list.pair + base, pairs, p.I, pitch, codes);
@@ -617,29 +635,25 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_down_kernel(const FewDownP
         quant.codes(mag, codes, scale, pitch);
         w4_lds_barrier();
     } else {
-        few_staged_barrier<kFewDepth>();
+        few_staged_barrier<D>();
     }
     int pair[NS], cnt = 0;
     float hs[NS];
-    auto tokens = [&](int c, const int8_t* (&cb)[NS]) {
-        cnt = __builtin_amdgcn_readfirstlane(list.count[c0 + c]);
-        const int first = list.first[c0 + c];
+    auto tokens = [&](const i32x4f_t& chunk, int (&cb)[NS]) {
+        cnt = __builtin_amdgcn_readfirstlane(chunk[2]);
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-            const int j = first + (s * 4 + r4 < cnt ? s * 4 + r4 : 0);
+            const int j = chunk[1] + (s * 4 + r4 < cnt ? s * 4 + r4 : 0);
             pair[s] = list.pair[j];
             hs[s] = scale[pair[s]];
-            cb[s] = codes + (SRC == kFewQuantise ? pair[s] : j - base) * pitch;
+            cb[s] = codes_at + (SRC == kFewQuantise ? pair[s] : j - base) * pitch;
         }
     };
-    auto done = [&](int it, i32x4f_t (&acc)[NS], const f32x2v_t& sc) {
-        const int r = lane >> 2;
-        if (r >= 4) return;
+    auto done = [&](int it, int (&sum)[NS], const f32x2v_t& sc) {
 #pragma unroll
-        for (int s = 0; s < NS; ++s) {
-            const int a = r == 0 ? acc[s][0] : (r == 1 ? acc[s][1] : (r == 2 ? acc[s][2] : acc[s][3]));
-            if (s * 4 + r4 < cnt) sums[(it * npairs + pair[s]) * 4 + r] = ((float)a * hs[s]) * sc[0];
-        }
+        for (int s = 0; s < NS; ++s)
+            if ((lane & 15) < 4 && s * 4 + r4 < cnt)
+                sums[(it * npairs + pair[s]) * 4 + few_row(lane)] = ((float)sum[s] * hs[s]) * sc[0];
     };
     for (;;) {
         work.run(ring, wv, p.I, slots, enter, row, scales, tokens, done);

@@ -10,17 +10,21 @@ namespace qlin {
 constexpr int kFewPairs = 256;   // 16 tokens, 16 slots
 constexpr int kFewThreads = 512, kFewWaves = kFewThreads / 64;  // one workgroup a compute unit: 16 waves, or two workgroups, are slower
 constexpr int kFewTokens = 16;   // tokens of a chunk at most: four column sets
-constexpr int kFewDepth = 4;     // steps of 256 K that a wave's loads are ahead of its products (a turn)
 constexpr int kFewUnitsPerWave = 6, kFewUnits = kFewUnitsPerWave * kFewWaves;  // x 512 elements that a workgroup quantises
 constexpr int kFewLds = 146 * 1024;  // dynamic LDS next to the lists, of 160 KB
 constexpr int kFewSums = 16 * 1024;  // of which the down projection's sums
 constexpr int kFewGrid = 256;        // compute units
 
-// LDS pitch of a code row: whole turns, and the four tokens of a column set 64 bytes (16 banks) apart
-constexpr int few_pitch(int64_t K) {
-    return (int)((K + 256 * kFewDepth - 1) / (256 * kFewDepth) * (256 * kFewDepth)) + 64;
+// A turn: steps of 256 K that a wave's loads are ahead of its products.  An item's K is a whole number of turns, so
+// three where that saves steps (K = 768: 3 instead of 4; 2064: 9 instead of 12).
+constexpr int few_turn(int64_t K) {
+    const int64_t steps = (K + 255) / 256;
+    return (steps + 2) / 3 * 3 < (steps + 3) / 4 * 4 ? 3 : 4;
 }
-static_assert(few_pitch(131072) <= kFewLds - kFewSums, "LDS holds the longest row");
+// LDS pitch of a code row: whole turns, and the four tokens of a column set 64 bytes (16 banks) apart
+constexpr int few_pitch(int64_t K, int turn) { return (int)((K + 256 * turn - 1) / (256 * turn)) * (256 * turn) + 64; }
+constexpr int few_pitch(int64_t K) { return few_pitch(K, few_turn(K)); }
+static_assert(few_pitch(131072) <= kFewLds - kFewSums && few_pitch(131072 - 16) <= kFewLds - kFewSums, "LDS holds the longest row");
 
 // All tokens' codes are in LDS at once.  (9 to 16 rows longer than that go to the GEMM.)
 constexpr bool few_fits(int64_t M, int64_t K) { return M <= kFewTokens && M * few_pitch(K) <= kFewLds; }
