@@ -29,43 +29,60 @@ hipError_t quantise(int dtype, const uint16_t* x, int64_t ldx, int64_t rows, int
     return hipGetLastError();
 }
 
-// One wave per token.
-template <int NR>
-__global__ __launch_bounds__(256) void i8_route_kernel(const float* logits, int64_t ldl, int M, int E, int topk, int route,
-                                                       int32_t* ids, float* gw) {
-    const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int lane = threadIdx.x & 63;
-    if (m >= M) return;
-    int id;
-    float w;
-    route_token<NR>(logits + m * ldl, E, topk, route, lane, id, w);
-    if (lane < topk) {
-        ids[m * topk + lane] = id;
-        gw[m * topk + lane] = w;
+// A workgroup a token: 8 waves quantise it, a ninth routes it (NR > 0).
+struct I8TokenParams {
+    const uint16_t* x; int64_t ldx; int64_t K; int8_t* xq; float* xs;
+    const float* logits; int64_t ldl; int E, topk, route; int32_t* ids; float* gw;
+};
+
+template <int T, int NR>
+__global__ __launch_bounds__(kI8QuantThreads + (NR > 0 ? 64 : 0)) void i8_token_kernel(const I8TokenParams p) {
+    const int64_t m = blockIdx.x;
+    if constexpr (NR > 0) {
+        if (threadIdx.x >= kI8QuantThreads) {
+            const int lane = threadIdx.x & 63;
+            int id;
+            float w;
+            route_token<NR>(p.logits + m * p.ldl, p.E, p.topk, p.route, lane, id, w);
+            if (lane < p.topk) {
+                p.ids[m * p.topk + lane] = id;
+                p.gw[m * p.topk + lane] = w;
+            }
+        }
     }
+    quantise_row_wg<T, kI8QuantThreads>(p.x + m * p.ldx, p.K, p.xq + m * p.K, p.xs + m);
 }
 
-hipError_t route(const I8MoeArgs& a, hipStream_t st) {
-    auto k = a.E <= 64 ? i8_route_kernel<1> : (a.E <= 128 ? i8_route_kernel<2> : (a.E <= 256 ? i8_route_kernel<4> : i8_route_kernel<16>));
-    hipLaunchKernelGGL(k, dim3((unsigned)((a.M + 3) / 4)), dim3(256), 0, st, a.logits, a.ldl, (int)a.M, (int)a.E,
-                       (int)a.topk, a.route, a.ids, a.gw);
-    return hipGetLastError();
-}
-
-// Pairs by expert: offs the first of each expert's pairs in perm, toffs the
-// first of its tiles of bm pairs.  One workgroup, LDS counters: the order of an
+// Pairs by expert (perm), and the row tiles of bm pairs that they make, each
+// with its expert.  One workgroup, LDS counters: the order of an
 // expert's pairs is arbitrary, which no result depends on (every pair's row is
-// computed on its own, the combine adds in slot order).
+// computed on its own, the combine adds in slot order).  A thread's ids are
+// loaded together, eight at a time, and kept where they are no more.
 constexpr int kI8MaxE = 1024;
 
-__device__ void sort_pairs(const int32_t* ids, int P, int E, int bm, int32_t* offs, int32_t* toffs, int32_t* perm) {
+__global__ __launch_bounds__(1024) void i8_sort_kernel(const int32_t* ids, int P, int E, int bm, I8Tile* tiles,
+                                                       int32_t* ntiles, int32_t* perm) {
     __shared__ int32_t cnt[kI8MaxE], cur[kI8MaxE], wsum[16], wtile[16];
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+    int32_t id[8];
+    auto load = [&](int base) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int p = base + i * 1024 + tid;
+            const int32_t e = ids[p < P ? p : P - 1];
+            id[i] = p < P && (uint32_t)e < (uint32_t)E ? e : -1;
+        }
+    };
+    load(0);
     cnt[tid] = 0;
     __syncthreads();
-    for (int p = tid; p < P; p += 1024) {
-        const int32_t e = ids[p];
-        if ((uint32_t)e < (uint32_t)E) atomicAdd(&cnt[e], 1);
+    for (int base = 0;;) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (id[i] >= 0) atomicAdd(&cnt[id[i]], 1);
+        base += 8192;
+        if (base >= P) break;
+        load(base);
     }
     __syncthreads();
     const int c = cnt[tid], t = (c + bm - 1) / bm;
@@ -88,50 +105,15 @@ __device__ void sort_pairs(const int32_t* ids, int P, int E, int bm, int32_t* of
         ti += wtile[q];
     }
     cur[tid] = ci - c;
-    if (tid <= E) {  // experts past E count nothing: entry E is the total
-        offs[tid] = ci - c;
-        toffs[tid] = ti - t;
-    }
-    if (tid == kI8MaxE - 1 && E == kI8MaxE) {
-        offs[E] = ci;
-        toffs[E] = ti;
-    }
+    for (int k = 0; k < t; ++k) tiles[ti - t + k] = I8Tile{tid, ti - t, ci - c, c};
+    if (tid == kI8MaxE - 1) *ntiles = ti;  // experts past E count nothing
     __syncthreads();
-    for (int p = tid; p < P; p += 1024) {
-        const int32_t e = ids[p];
-        if ((uint32_t)e < (uint32_t)E) perm[atomicAdd(&cur[e], 1)] = p;
+    for (int base = 0; base < P; base += 8192) {
+        if (P > 8192) load(base);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (id[i] >= 0) perm[atomicAdd(&cur[id[i]], 1)] = base + i * 1024 + tid;
     }
-}
-
-// Workgroups ahead of the last quantise a token each; the last one sorts the
-// pairs and, NR > 0, routes the tokens first.
-struct I8PrepParams {
-    const uint16_t* x; int64_t ldx; int64_t M; int64_t K; int8_t* xq; float* xs;
-    const float* logits; int64_t ldl; int E, topk, route, bm;
-    int32_t* ids; float* gw; int32_t *offs, *toffs, *perm;
-};
-
-template <int T, int NR>
-__global__ __launch_bounds__(1024) void i8_prep_kernel(const I8PrepParams p) {
-    const int64_t m = blockIdx.x;
-    if (m < p.M) {
-        quantise_row_wg<T, 1024>(p.x + m * p.ldx, p.K, p.xq + m * p.K, p.xs + m);
-        return;
-    }
-    if constexpr (NR > 0) {
-        const int lane = threadIdx.x & 63;
-        for (int t = threadIdx.x >> 6; t < p.M; t += 16) {
-            int id;
-            float w;
-            route_token<NR>(p.logits + t * p.ldl, p.E, p.topk, p.route, lane, id, w);
-            if (lane < p.topk) {
-                p.ids[t * p.topk + lane] = id;
-                p.gw[t * p.topk + lane] = w;
-            }
-        }
-        __syncthreads();  // the ids are read back by other threads of this workgroup
-    }
-    sort_pairs(p.ids, (int)p.M * p.topk, p.E, p.bm, p.offs, p.toffs, p.perm);
 }
 
 // y[t,n] = r16(sum_j gw[t,j] part[t,j,n]) in slot order, four columns a thread.
@@ -169,7 +151,7 @@ hipError_t run_gemm(I8GemmParams p, int64_t row_tiles, int64_t first, int64_t co
 // row tiles that P pairs of E groups can make at most
 int64_t most_tiles(int64_t P, int64_t E, int64_t bm) { return P / bm + (E < P ? E : P); }
 
-struct MoeRegions { size_t xq, xs, h, hq, hs, part, offs, toffs, perm, list, total; };
+struct MoeRegions { size_t xq, xs, h, hq, hs, part, tiles, ntiles, perm, list, total; };
 
 MoeRegions regions(int64_t M, int64_t H, int64_t I, int64_t topk, int64_t E) {
     MoeRegions r{};
@@ -186,8 +168,8 @@ MoeRegions regions(int64_t M, int64_t H, int64_t I, int64_t topk, int64_t E) {
     r.hq = take(P * I);
     r.hs = take(P * 4);
     r.part = take(P * H * 4);
-    r.offs = take((E + 1) * 4);
-    r.toffs = take((E + 1) * 4);
+    r.tiles = take(most_tiles(P, E, 64) * (int64_t)sizeof(I8Tile));
+    r.ntiles = take(4);
     r.perm = take(P * 4);
     r.list = take((int64_t)few_list_bytes());
     r.total = at;
@@ -202,35 +184,38 @@ hipError_t moe(const I8MoeArgs& a, hipStream_t st) {
     int8_t *xq = (int8_t*)(ws + r.xq), *hq = (int8_t*)(ws + r.hq);
     float *xs = (float*)(ws + r.xs), *hs = (float*)(ws + r.hs), *part = (float*)(ws + r.part);
     uint16_t* h = (uint16_t*)(ws + r.h);
-    int32_t *offs = (int32_t*)(ws + r.offs), *toffs = (int32_t*)(ws + r.toffs), *perm = (int32_t*)(ws + r.perm);
+    I8Tile* tiles = (I8Tile*)(ws + r.tiles);
+    int32_t *ntiles = (int32_t*)(ws + r.ntiles), *perm = (int32_t*)(ws + r.perm);
     if (few_fits(a.M, a.H)) {
         const I8FewRegions f{xq, xs, h, hq, hs, ws + r.list};
         return T == kFp16 ? few_moe_fp16(a, f, st) : few_moe_bf16(a, f, st);
     }
     const int bm = (int)i8_tile_rows(P, a.E);
-    const bool one = a.logits && a.M <= kI8PrepTokens;  // one launch routes, sorts and quantises
-    hipError_t e = a.logits && !one ? route(a, st) : hipSuccess;
+    const I8TokenParams q{a.x, a.ldx, a.H, xq, xs, a.logits, a.ldl, (int)a.E, (int)a.topk, a.route, a.ids, a.gw};
+    auto token = !a.logits ? i8_token_kernel<T, 0>
+                           : (a.E <= 64 ? i8_token_kernel<T, 1>
+                                        : (a.E <= 128 ? i8_token_kernel<T, 2>
+                                                      : (a.E <= 256 ? i8_token_kernel<T, 4> : i8_token_kernel<T, 16>)));
+    hipLaunchKernelGGL(token, dim3((unsigned)a.M), dim3(kI8QuantThreads + (a.logits ? 64 : 0)), 0, st, q);
+    hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const I8PrepParams q{a.x, a.ldx, a.M, a.H, xq, xs, a.logits, a.ldl, (int)a.E, (int)a.topk, a.route, bm,
-                         a.ids, a.gw, offs, toffs, perm};
-    auto prep = !one ? i8_prep_kernel<T, 0> : (a.E <= 128 ? i8_prep_kernel<T, 2> : i8_prep_kernel<T, 16>);
-    hipLaunchKernelGGL(prep, dim3((unsigned)a.M + 1), dim3(1024), 0, st, q);
+    hipLaunchKernelGGL(i8_sort_kernel, dim3(1), dim3(1024), 0, st, a.ids, (int)P, (int)a.E, bm, tiles, ntiles, perm);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     I8GemmParams g{};
-    g.x = xq; g.ldx = a.H; g.xs = xs; g.offs = offs; g.toffs = toffs; g.perm = perm; g.div = (int)a.topk; g.E = (int)a.E;
+    g.x = xq; g.ldx = a.H; g.xs = xs; g.tiles = tiles; g.ntiles = ntiles; g.perm = perm; g.div = (int)a.topk;
     g.K = a.H; g.w = a.w13; g.ldw = a.ldw13; g.N = 2 * a.I; g.ws = a.s13; g.ws_step = 1; g.C = a.I; g.act = a.act;
     g.y = h; g.ldy = a.I;
-    const int64_t tiles = most_tiles(P, a.E, bm);
-    e = bm == 64 ? run_gemm<T, kI8Gated, 128, 64, 2, 2>(g, tiles, 0, a.I, st)
-                 : run_gemm<T, kI8Gated, 128, 128, 2, 4>(g, tiles, 0, a.I, st);
+    const int64_t most = most_tiles(P, a.E, bm);
+    e = bm == 64 ? run_gemm<T, kI8Gated, 128, 64, 2, 2>(g, most, 0, a.I, st)
+                 : run_gemm<T, kI8Gated, 128, 128, 2, 4>(g, most, 0, a.I, st);
     if (e != hipSuccess) return e;
     e = quantise(T, h, a.I, P, a.I, hq, a.I, hs, a.ids, a.E, st);
     if (e != hipSuccess) return e;
     g.x = hq; g.ldx = a.I; g.xs = hs; g.div = 1; g.K = a.I; g.w = a.w2; g.ldw = a.ldw2; g.N = a.H; g.ws = a.s2;
     g.C = a.H; g.y = nullptr; g.part = part; g.ldy = a.H;
-    e = bm == 64 ? run_gemm<T, kI8Part, 128, 64, 4, 2>(g, tiles, 0, a.H, st)
-                 : run_gemm<T, kI8Part, 128, 128, 2, 4>(g, tiles, 0, a.H, st);
+    e = bm == 64 ? run_gemm<T, kI8Part, 128, 64, 4, 2>(g, most, 0, a.H, st)
+                 : run_gemm<T, kI8Part, 128, 128, 2, 4>(g, most, 0, a.H, st);
     if (e != hipSuccess) return e;
     const int64_t n = a.M * (a.H / 4);
     hipLaunchKernelGGL(i8_combine_kernel<T>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, part, a.ids, a.gw, a.M,
@@ -244,7 +229,7 @@ hipError_t glu(const I8GluArgs& a, hipStream_t st) {
     const hipError_t e = quantise(T, a.x, a.ldx, a.M, a.K, a.xq, a.ldxq, a.xs, nullptr, 0, st);
     if (e != hipSuccess) return e;
     I8GemmParams g{};
-    g.x = a.xq; g.ldx = a.ldxq; g.xs = a.xs; g.R = a.M; g.E = 1; g.div = 1;
+    g.x = a.xq; g.ldx = a.ldxq; g.xs = a.xs; g.R = a.M; g.div = 1;
     g.K = a.K; g.w = a.w13; g.ldw = a.ldw; g.N = 2 * a.I; g.ws = a.s13; g.ws_step = a.ws_step; g.C = a.I; g.act = a.act;
     g.y = a.y; g.ldy = a.ldy;
     if (i8_dense_rows(a.M) == 64) return run_gemm<T, kI8Gated, 128, 64, 2, 2>(g, 1, 0, a.I, st);

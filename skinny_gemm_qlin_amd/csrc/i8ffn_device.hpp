@@ -94,13 +94,13 @@ __device__ __forceinline__ uint2 codes8(const u32x4_t& v, const RowScale& o) {
     return make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
 }
 
-// A workgroup of NT threads quantises a row: largest magnitude, then codes.
+// The first NT threads of a workgroup quantise a row: largest magnitude, then codes.  All threads call it (a barrier).
 template <int T, int NT>
 __device__ __forceinline__ void quantise_row_wg(const uint16_t* row, int64_t K, int8_t* out, float* scale) {
     constexpr int W = NT / 64, CACHED = 2;
     __shared__ uint32_t part[W];
     const int tid = threadIdx.x;
-    const int64_t nvec = K >> 3;
+    const int64_t nvec = tid < NT ? K >> 3 : 0;
     u32x4_t cache[CACHED];
     uint32_t a = 0;
 #pragma unroll
@@ -111,7 +111,7 @@ __device__ __forceinline__ void quantise_row_wg(const uint16_t* row, int64_t K, 
     }
     for (int64_t i = tid + CACHED * NT; i < nvec; i += NT) a = mag8(ld16(row + i * 8), a);
     a = wave_mag(a);
-    if ((tid & 63) == 0) part[tid >> 6] = a;
+    if ((tid & 63) == 0 && tid < NT) part[tid >> 6] = a;
     __syncthreads();
     uint32_t mag = part[0];
 #pragma unroll

@@ -18,12 +18,14 @@ namespace qlin {
 
 enum I8Epi { kI8Gated = 0, kI8Part = 1 };
 
+// The group (expert) that a row tile belongs to: its first row tile, first row and number of rows.
+struct I8Tile { int group, tile, row, rows; };
+
 struct I8GemmParams {
     const int8_t* x; int64_t ldx; const float* xs;  // codes [rows][ldx] and their scales
     int64_t R;                                      // dense: rows
-    const int32_t* offs; const int32_t* toffs;      // grouped: first row of each group, first tile of each group [E + 1]
+    const I8Tile* tiles; const int32_t* ntiles;     // grouped: of each row tile its group; null: dense
     const int32_t* perm; int div;                   // grouped: row r of the groups is pair perm[r], code row perm[r] / div
-    int E;                                          // groups (1: dense, offs null)
     int64_t K; const int8_t* w; int64_t ldw; int64_t N;  // N weight rows a group (gated: 2 I)
     const float* ws; int ws_step;                   // [E][N]
     int64_t C;                                      // output columns: I or N
@@ -46,7 +48,7 @@ __device__ __forceinline__ void i8_stage_barrier() {
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
-constexpr int64_t kI8BandM = 8;  // row tiles per raster band
+constexpr int kI8BandM = 8;  // row tiles per raster band
 
 template <int T, int EPI, int BN, int BM, int WGN, int WGM>
 __global__ __launch_bounds__(64 * WGM * WGN, WGM * WGN == 16 ? 4 : 2) void i8_gemm_kernel(const I8GemmParams p) {
@@ -58,38 +60,33 @@ __global__ __launch_bounds__(64 * WGM * WGN, WGM * WGN == 16 ? 4 : 2) void i8_ge
     static_assert(TM >= 1 && TN >= 1 && XI >= 1 && WI >= 1 && (EPI != kI8Gated || TN % 2 == 0), "tile");
     // an object of its own for each tile: a load into one need not be waited for before another is read
     __shared__ __align__(16) uint8_t x_even[XT], x_odd[XT], w_even[WT], w_odd[WT];
-    __shared__ int32_t rows[BM];  // grouped: the tile's pairs
+    __shared__ int32_t rows[BM];  // the tile's output rows, their codes' scales: no load between the stores of the end
+    __shared__ float scale[BM];
 
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-    const int64_t tiles_c = (p.c_count + CT - 1) / CT;
+    const int tiles_c = (int)((p.c_count + CT - 1) / CT);
     int64_t c0, m0, cnt;  // first column; first row and number of rows of the tile
     int e = 0;
     const int b = blockIdx.x;
-    if (p.offs) {
+    if (p.tiles) {
         // an XCD (workgroups are dealt to the 8 of them in turn) takes a run of the tiles that the routing made:
         // expert by expert, column tile by column tile, the row tiles that share it next to each other
-        const int64_t tiles = p.toffs[p.E] * tiles_c, per = (tiles + 7) / 8;
-        const int64_t t = (int64_t)(b % 8) * per + b / 8;
-        if (b / 8 >= per || t >= tiles) return;  // workgroup-uniform
-        int lo = 0, hi = p.E;  // largest e with toffs[e] * tiles_c <= t
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (p.toffs[mid] * tiles_c <= t) lo = mid;
-            else hi = mid;
-        }
-        e = lo;
-        const int64_t mt = p.toffs[e + 1] - p.toffs[e], rr = t - p.toffs[e] * tiles_c;
-        c0 = p.c_first + rr / mt * CT;
-        m0 = p.offs[e] + rr % mt * BM;
-        cnt = p.offs[e + 1] - m0;
+        const int tiles = *p.ntiles * tiles_c, per = (tiles + 7) / 8, t = (b & 7) * per + (b >> 3);
+        if ((b >> 3) >= per || t >= tiles) return;  // workgroup-uniform
+        const I8Tile g = p.tiles[t / tiles_c];  // some row tile of the group
+        e = g.group;
+        const int mt = (g.rows + BM - 1) / BM, rr = t - g.tile * tiles_c, ct = rr / mt, rt = rr - ct * mt;
+        c0 = p.c_first + (int64_t)ct * CT;
+        m0 = g.row + rt * BM;
+        cnt = g.rows - rt * BM;
     } else {
-        const int64_t tiles_m = (p.R + BM - 1) / BM, tiles = tiles_m * tiles_c, per = (tiles + 7) / 8;
-        const int64_t t = (int64_t)(b % 8) * per + b / 8;
-        if (b / 8 >= per || t >= tiles) return;  // workgroup-uniform
-        const int64_t bsz = kI8BandM * tiles_c, band = t / bsz, rr = t - band * bsz;
-        const int64_t gm = tiles_m - band * kI8BandM < kI8BandM ? tiles_m - band * kI8BandM : kI8BandM;
-        c0 = p.c_first + rr / gm * CT;
-        m0 = (band * kI8BandM + rr % gm) * BM;
+        const int tiles_m = (int)((p.R + BM - 1) / BM), tiles = tiles_m * tiles_c, per = (tiles + 7) / 8;
+        const int t = (b & 7) * per + (b >> 3);
+        if ((b >> 3) >= per || t >= tiles) return;  // workgroup-uniform
+        const int bsz = kI8BandM * tiles_c, band = t / bsz, rr = t - band * bsz;
+        const int gm = tiles_m - band * kI8BandM < kI8BandM ? tiles_m - band * kI8BandM : kI8BandM, ct = rr / gm;
+        c0 = p.c_first + (int64_t)ct * CT;
+        m0 = (int64_t)(band * kI8BandM + rr - ct * gm) * BM;
         cnt = p.R - m0;
     }
     const int rows_here = cnt < BM ? (int)cnt : BM;
@@ -105,7 +102,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, WGM * WGN == 16 ? 4 : 2) void i8_ge
         const int r = (wv * XI + i) * 8 + (lane >> 3);
         const int rc = r < rows_here ? r : rows_here - 1;  // rows past the group: clamped, not stored
         int64_t src = m0 + rc;
-        if (p.offs) src = p.perm[src] / p.div;
+        if (p.tiles) src = p.perm[src] / p.div;
         xcol[i] = ((lane & 7) ^ i8_swz(r)) * 16;
         xsrc[i] = (const uint8_t*)p.x + src * p.ldx + xcol[i];
     }
@@ -122,8 +119,12 @@ __global__ __launch_bounds__(64 * WGM * WGN, WGM * WGN == 16 ? 4 : 2) void i8_ge
         wcol[i] = ((lane & 7) ^ i8_swz(r)) * 16;
         wsrc[i] = (const uint8_t*)w + n * p.ldw + wcol[i];
     }
-    if (p.offs)
-        for (int i = tid; i < BM; i += 64 * NW) rows[i] = p.perm[m0 + (i < rows_here ? i : rows_here - 1)];
+    for (int i = tid; i < BM; i += 64 * NW) {
+        const int64_t at = m0 + (i < rows_here ? i : rows_here - 1);
+        const int pair = p.tiles ? p.perm[at] : (int)at;
+        rows[i] = pair;
+        scale[i] = p.xs[p.tiles ? pair / p.div : pair];
+    }
     auto issue = [&](int64_t s, uint8_t* xt, uint8_t* wt) {  // chunks past K are zeros
 #pragma unroll
         for (int i = 0; i < XI; ++i) {
@@ -188,28 +189,31 @@ __global__ __launch_bounds__(64 * WGM * WGN, WGM * WGN == 16 ? 4 : 2) void i8_ge
     w4_wait_vmcnt<0>();  // no load into LDS outlives the workgroup
 
     // register v of a 32 x 32 tile holds code row 8(v/4) + 4*half + v%4, weight row lane%32
+    constexpr int NC = EPI == kI8Gated ? TN / 2 : TN;  // output columns of a lane
+    constexpr int CW = EPI == kI8Gated ? BN / WGN / 2 : BN / WGN;
+    const int64_t cl = c0 + wn * CW + row;
+    float sc[NC], su[NC];
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+        const int64_t c = cl + j * 32 < C ? cl + j * 32 : C - 1;
+        sc[j] = ws[c * p.ws_step];
+        su[j] = EPI == kI8Gated ? ws[(C + c) * p.ws_step] : 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
             const int r = wm * (BM / WGM) + i * 32 + 8 * (v >> 2) + 4 * half + (v & 3);
             if (r >= rows_here) continue;
-            const int64_t pair = p.offs ? rows[r] : m0 + r;
-            const float xs = p.xs[p.offs ? pair / p.div : pair];
-            if constexpr (EPI == kI8Gated) {
+            const int64_t at = (int64_t)rows[r] * p.ldy + cl;
+            const float xs = scale[r];
 #pragma unroll
-                for (int j = 0; j < TN; j += 2) {
-                    const int64_t c = c0 + wn * (BN / WGN / 2) + j / 2 * 32 + row;
-                    if (c < C)
-                        p.y[pair * p.ldy + c] = f32_to_h<T>(gated(acc[i][j][v], acc[i][j + 1][v], xs, ws[c * p.ws_step],
-                                                                  ws[(C + c) * p.ws_step], p.act));
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < TN; ++j) {
-                    const int64_t c = c0 + wn * (BN / WGN) + j * 32 + row;
-                    if (c < C) p.part[pair * p.ldy + c] = ((float)acc[i][j][v] * xs) * ws[c * p.ws_step];
-                }
+            for (int j = 0; j < NC; ++j) {
+                if (cl + j * 32 >= C) continue;
+                if constexpr (EPI == kI8Gated)
+                    p.y[at + j * 32] = f32_to_h<T>(gated(acc[i][2 * j][v], acc[i][2 * j + 1][v], xs, sc[j], su[j], p.act));
+                else
+                    p.part[at + j * 32] = ((float)acc[i][j][v] * xs) * sc[j];
             }
         }
 }

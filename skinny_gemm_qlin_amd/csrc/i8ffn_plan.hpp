@@ -64,7 +64,4 @@ constexpr int64_t i8_large_columns(int64_t M, int64_t I) {
     return rounds * 256 / mt * 128;
 }
 
-// Tokens up to which one workgroup routes all of them and sorts the pairs, next to the ones that quantise them.
-constexpr int64_t kI8PrepTokens = 64;
-
 }  // namespace qlin
