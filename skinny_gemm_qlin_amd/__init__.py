@@ -587,25 +587,34 @@ def qlin_glu_w4_bwd(dy, w13, s13, z13=None, act=QLIN_ACT_SILU, x=None, gu=None, 
 
 
 # ----------------------------------------------------------------------------- INT8 feed-forward
+# As with the 4-bit calls, each tensor is looked at once; the functions named _..._wrong say what a failed check saw.
 
 def _operand(t, name, dtype, shape, dev, dense=True):
-    """An operand of a type, shape and device; rows contiguous, or with dense=False of any pitch."""
-    try:
-        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev
-                and (t.is_contiguous() if dense else t.stride(-1) == 1 or shape[-1] == 1)):
-            return t
-    except (AttributeError, RuntimeError):  # no tensor, or no strided one
-        pass
+    """Raises unless t has this type, shape and device, and contiguous rows (dense: is contiguous)."""
     _need(t, name, (dtype,), len(shape))
-    raise ValueError(f"{name} must be {'contiguous ' if dense else ''}{tuple(shape)} on cuda:{dev}, got {tuple(t.shape)} "
-                     f"(strides {t.stride()}) on {t.device}")
+    if tuple(t.shape) != tuple(shape) or t.get_device() != dev or not (t.is_contiguous() or not dense):
+        raise ValueError(f"{name} must be {'contiguous ' if dense else ''}{tuple(shape)} on cuda:{dev}, got "
+                         f"{tuple(t.shape)} (strides {t.stride()}) on {t.device}")
 
 
-def _x16(x):
-    """The 16-bit activations of a call: (rows, row length, dtype flag, device index)."""
-    if not isinstance(x, torch.Tensor) or x.dtype not in _DT16 or x.dim() != 2 or not x.is_cuda or x.stride(1) != 1:
-        _need(x, "x", tuple(_DT16), 2)
-    return x.shape[0], x.shape[1], _DT16[x.dtype], x.get_device()
+def _glu_i8_wrong(x, w13, s13, xq, xs, y):
+    _need(x, "x", tuple(_DT16), 2)
+    M, K = x.shape
+    dev = x.get_device()
+    _need(w13, "w13", (torch.int8,), 2)
+    N = w13.shape[0]
+    _operand(w13, "w13", torch.int8, (N, K), dev, False)
+    if N % 2:
+        raise ValueError(f"w13 has {N} rows: 2I are needed")
+    _need(s13, "s13", (torch.float32,), 1)
+    _operand(s13, "s13", torch.float32, (1,) if s13.numel() == 1 else (N,), dev)
+    if xq is not None:
+        _operand(xq, "xq", torch.int8, (M, K), dev, False)
+    if xs is not None:
+        _operand(xs, "xs", torch.float32, (M,), dev)
+    if y is not None:
+        _operand(y, "y", x.dtype, (M, N // 2), dev, False)
+    raise ValueError("qlin_glu_i8: operands that are no plain strided tensors")
 
 
 def qlin_glu_i8(x, w13, s13, act=QLIN_ACT_SILU, xq=None, xs=None, y=None, stream=None):
@@ -613,20 +622,35 @@ def qlin_glu_i8(x, w13, s13, act=QLIN_ACT_SILU, xq=None, xs=None, y=None, stream
     [2I, K] (gate rows, then up rows; any row pitch that is a multiple of 16); s13
     fp32 [2I] or [1].  x is quantised per token (codes and scales into xq int8 [M, K]
     / xs fp32 [M]).  Returns (y [M, I] of x's dtype, xq, xs)."""
-    M, K, dt, dev = _x16(x)
-    _operand(w13, "w13", torch.int8, (w13.shape[0] if isinstance(w13, torch.Tensor) and w13.dim() == 2 else 0, K), dev,
-             False)
-    N = w13.shape[0]
-    if N % 2:
-        raise ValueError(f"w13 has {N} rows: 2I are needed")
-    _operand(s13, "s13", torch.float32, (1,) if isinstance(s13, torch.Tensor) and s13.numel() == 1 else (N,), dev)
-    xq = (_own(None, (M, K), torch.int8, x, stream) if xq is None
-          else _operand(xq, "xq", torch.int8, (M, K), dev, False))
-    xs = _own(None, (M,), torch.float32, x, stream) if xs is None else _operand(xs, "xs", torch.float32, (M,), dev)
-    y = _own(None, (M, N // 2), x.dtype, x, stream) if y is None else _operand(y, "y", x.dtype, (M, N // 2), dev, False)
-    _launch(load().qlin_glu_i8, "qlin_glu_i8", dev, stream, x.data_ptr(), _pitch(x, M, K), M, K, dt, w13.data_ptr(),
-            _wpitch(w13), N // 2, s13.data_ptr(), int(s13.shape[0] > 1), act, xq.data_ptr(),
-            xq.stride(0) if M > 1 else K, xs.data_ptr(), y.data_ptr(), _pitch(y, M, N // 2))
+    try:
+        dt, dtype, dev = _DT16.get(x.dtype), x.dtype, x.get_device()
+        M, K = x.shape
+        N, Kw = w13.shape
+        ns, = s13.shape
+        I = N // 2
+        ok = (dt is not None and dev >= 0 and Kw == K and 2 * I == N and (ns == N or ns == 1)
+              and w13.dtype is torch.int8 and s13.dtype is torch.float32
+              and w13.get_device() == dev == s13.get_device() and s13.is_contiguous()
+              and (x.stride(1) == 1 or K == 1) and (w13.stride(1) == 1 or K == 1)
+              and (xq is None or (xq.dtype is torch.int8 and xq.shape == x.shape and xq.get_device() == dev
+                                  and (xq.stride(1) == 1 or K == 1)))
+              and (xs is None or (xs.dtype is torch.float32 and xs.shape == (M,) and xs.get_device() == dev
+                                  and xs.is_contiguous()))
+              and (y is None or (y.dtype is dtype and y.shape == (M, I) and y.get_device() == dev
+                                 and (y.stride(1) == 1 or I == 1))))
+    except (AttributeError, ValueError, TypeError, IndexError, RuntimeError):  # something here is no such tensor
+        ok = False
+    if not ok:
+        _glu_i8_wrong(x, w13, s13, xq, xs, y)
+    if xq is None:
+        xq = _own(None, (M, K), torch.int8, x, stream)
+    if xs is None:
+        xs = _own(None, (M,), torch.float32, x, stream)
+    if y is None:
+        y = _own(None, (M, I), dtype, x, stream)
+    _launch(load().qlin_glu_i8, "qlin_glu_i8", dev, stream, x.data_ptr(), x.stride(0) if M > 1 else (K + 7) // 8 * 8, M, K,
+            dt, w13.data_ptr(), w13.stride(0) if N > 1 else K, I, s13.data_ptr(), 1 if ns > 1 else 0, act, xq.data_ptr(),
+            xq.stride(0) if M > 1 else K, xs.data_ptr(), y.data_ptr(), y.stride(0) if M > 1 else I)
     return y, xq, xs
 
 
@@ -634,14 +658,48 @@ def qlin_moe_ffn_i8_workspace_bytes(M: int, H: int, I: int, topk: int, E: int) -
     return int(load().qlin_moe_ffn_i8_workspace_bytes(M, H, I, topk, E))
 
 
-def _experts(w, name, rows, cols, dev):
-    """Expert matrices int8 [E, rows, cols]: any row pitch, the experts one behind the other; returns the row pitch."""
-    _operand(w, name, torch.int8, (w.shape[0] if isinstance(w, torch.Tensor) and w.dim() == 3 else 0, rows, cols), dev,
-             False)
-    pitch = w.stride(1) if rows > 1 else (w.stride(0) if w.shape[0] > 1 else cols)
-    if w.shape[0] > 1 and w.stride(0) != rows * pitch:
-        raise ValueError(f"{name}: the experts must lie one behind the other, strides {w.stride()}")
-    return pitch
+def _expert_pitch(w):
+    """Row pitch of expert matrices [E, rows, cols] that lie one behind the other, else None."""
+    E, rows, cols = w.shape
+    s0, s1, s2 = w.stride()
+    if s2 != 1 and cols > 1:
+        return None
+    if rows == 1:
+        s1 = s0 if E > 1 else cols
+    return s1 if E == 1 or s0 == rows * s1 else None
+
+
+def _moe_i8_wrong(x, w13, s13, w2, s2, logits, topk, ids, gw, y, workspace):
+    _need(x, "x", tuple(_DT16), 2)
+    M, H = x.shape
+    dev = x.get_device()
+    _need(w13, "w13", (torch.int8,), 3)
+    _need(w2, "w2", (torch.int8,), 3)
+    E, I = w13.shape[0], w2.shape[2]
+    for name, w, rows, cols in (("w13", w13, 2 * I, H), ("w2", w2, H, I)):
+        _operand(w, name, torch.int8, (E, rows, cols), dev, False)
+        if _expert_pitch(w) is None:
+            raise ValueError(f"{name}: rows must be contiguous and the experts lie one behind the other, strides {w.stride()}")
+    _operand(s13, "s13", torch.float32, (E, 2 * I), dev)
+    _operand(s2, "s2", torch.float32, (E, H), dev)
+    if logits is None:
+        if ids is None or gw is None:
+            raise ValueError("either logits or ids and gw are needed")
+        _need(ids, "ids", (torch.int32,), 2)
+        topk = ids.shape[1] if topk is None else topk
+    else:
+        if not isinstance(topk, int):
+            raise ValueError("topk, an int, is needed along with logits")
+        _operand(logits, "logits", torch.float32, (M, E), dev, False)
+    for name, t, dtype in (("ids", ids, torch.int32), ("gw", gw, torch.float32)):
+        if t is not None:
+            _operand(t, name, dtype, (M, topk), dev)
+    if y is not None:
+        _operand(y, "y", x.dtype, (M, H), dev, False)
+    if workspace is not None and not (isinstance(workspace, torch.Tensor) and workspace.get_device() == dev
+                                      and workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {x.device}")
+    raise ValueError("qlin_moe_ffn_i8: operands that are no plain strided tensors")
 
 
 def qlin_moe_ffn_i8(x, w13, s13, w2, s2, logits=None, topk=None, route=QLIN_ROUTE_SELECTED, act=QLIN_ACT_SILU, ids=None,
@@ -652,38 +710,46 @@ def qlin_moe_ffn_i8(x, w13, s13, w2, s2, logits=None, topk=None, route=QLIN_ROUT
     on the device (NaN and -inf mask an expert) and written to ids int32 [M, topk] / gw
     fp32 [M, topk].  Without logits ids and gw are inputs; an id outside the experts
     contributes nothing.  Returns (y [M, H] of x's dtype, ids, gw)."""
-    M, H, dt, dev = _x16(x)
-    if not isinstance(w13, torch.Tensor) or not isinstance(w2, torch.Tensor) or w13.dim() != 3 or w2.dim() != 3:
-        _need(w13, "w13", (torch.int8,), 3)
-        _need(w2, "w2", (torch.int8,), 3)
-    E, I = w13.shape[0], w2.shape[2]
-    p13, p2 = _experts(w13, "w13", 2 * I, H, dev), _experts(w2, "w2", H, I, dev)
-    if w2.shape[0] != E:
-        raise ValueError(f"w13 has {E} experts, w2 {w2.shape[0]}")
-    _operand(s13, "s13", torch.float32, (E, 2 * I), dev)
-    _operand(s2, "s2", torch.float32, (E, H), dev)
-    if logits is not None:
-        if topk is None:
-            raise ValueError("topk is needed along with logits")
-        _operand(logits, "logits", torch.float32, (M, E), dev, False)
-        ids = _own(None, (M, topk), torch.int32, x, stream) if ids is None else _operand(ids, "ids", torch.int32, (M, topk), dev)
-        gw = _own(None, (M, topk), torch.float32, x, stream) if gw is None else _operand(gw, "gw", torch.float32, (M, topk), dev)
-    else:
-        if ids is None or gw is None:
-            raise ValueError("either logits or ids and gw are needed")
-        if topk is None and isinstance(ids, torch.Tensor) and ids.dim() == 2:
+    try:
+        dt, dtype, dev = _DT16.get(x.dtype), x.dtype, x.get_device()
+        M, H = x.shape
+        E, N, Hw = w13.shape
+        E2, H2, I = w2.shape
+        if logits is None and topk is None:
             topk = ids.shape[1]
-        _operand(ids, "ids", torch.int32, (M, topk), dev)
-        _operand(gw, "gw", torch.float32, (M, topk), dev)
-    y = _own(None, (M, H), x.dtype, x, stream) if y is None else _operand(y, "y", x.dtype, (M, H), dev, False)
+        p13, p2, slots = _expert_pitch(w13), _expert_pitch(w2), (M, topk)
+        ok = (dt is not None and dev >= 0 and Hw == H == H2 and E2 == E and N == 2 * I
+              and p13 is not None and p2 is not None and (x.stride(1) == 1 or H == 1)
+              and w13.dtype is torch.int8 and w2.dtype is torch.int8 and s13.dtype is torch.float32
+              and s2.dtype is torch.float32 and s13.shape == (E, N) and s2.shape == (E, H)
+              and w13.get_device() == dev == w2.get_device() and s13.get_device() == dev == s2.get_device()
+              and s13.is_contiguous() and s2.is_contiguous()
+              and (logits is not None or (ids is not None and gw is not None))
+              and (logits is None or (logits.dtype is torch.float32 and logits.shape == (M, E)
+                                      and logits.get_device() == dev and (logits.stride(1) == 1 or E == 1)
+                                      and isinstance(topk, int)))
+              and (ids is None or (ids.dtype is torch.int32 and ids.shape == slots and ids.get_device() == dev
+                                   and ids.is_contiguous()))
+              and (gw is None or (gw.dtype is torch.float32 and gw.shape == slots and gw.get_device() == dev
+                                  and gw.is_contiguous()))
+              and (y is None or (y.dtype is dtype and y.shape == (M, H) and y.get_device() == dev
+                                 and (y.stride(1) == 1 or H == 1)))
+              and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous())))
+    except (AttributeError, ValueError, TypeError, IndexError, RuntimeError):  # something here is no such tensor
+        ok = False
+    if not ok:
+        _moe_i8_wrong(x, w13, s13, w2, s2, logits, topk, ids, gw, y, workspace)
     lib = load()
     if workspace is None:
-        need = lib.qlin_moe_ffn_i8_workspace_bytes(M, H, I, topk, E)
-        workspace = _own(None, (max(need, 1),), torch.uint8, x, stream)
-    elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {x.device}")
-    _launch(lib.qlin_moe_ffn_i8, "qlin_moe_ffn_i8", dev, stream, x.data_ptr(), _pitch(x, M, H), M, H, dt,
-            _ptr(logits), 0 if logits is None else (logits.stride(0) if M > 1 else E), E, topk, route, w13.data_ptr(), p13,
-            s13.data_ptr(), I, w2.data_ptr(), p2, s2.data_ptr(), act, ids.data_ptr(), gw.data_ptr(), y.data_ptr(),
-            _pitch(y, M, H), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        workspace = _own(None, (max(lib.qlin_moe_ffn_i8_workspace_bytes(M, H, I, topk, E), 1),), torch.uint8, x, stream)
+    if ids is None:
+        ids = _own(None, slots, torch.int32, x, stream)
+    if gw is None:
+        gw = _own(None, slots, torch.float32, x, stream)
+    if y is None:
+        y = _own(None, (M, H), dtype, x, stream)
+    _launch(lib.qlin_moe_ffn_i8, "qlin_moe_ffn_i8", dev, stream, x.data_ptr(), x.stride(0) if M > 1 else (H + 7) // 8 * 8, M,
+            H, dt, None if logits is None else logits.data_ptr(), E if logits is None or M == 1 else logits.stride(0), E,
+            topk, route, w13.data_ptr(), p13, s13.data_ptr(), I, w2.data_ptr(), p2, s2.data_ptr(), act, ids.data_ptr(),
+            gw.data_ptr(), y.data_ptr(), y.stride(0) if M > 1 else H, workspace.data_ptr(), workspace.nbytes)
     return y, ids, gw
