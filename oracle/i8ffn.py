@@ -66,6 +66,9 @@ def front(q, s, w13, s13, kind, dt):
     fp32 = np.abs(u) * (da * np.abs(g) * e + np.abs(a) * (2.0 ** -20 + e)) + np.abs(y) * 2.0 ** -23
     v = np.abs(g) if kind == 0 else 1.6 * np.abs(g) * (1 + 0.045 * g ** 2)
     fp32 += np.abs(y) * np.minimum(v, 90.0) * 4 * 2.0 ** -23  # act's relative change with an error in v
+    # the logistic is taken from an exponential in (0, 1] whose result the hardware gives as 0 below 2^-126, the smallest
+    # normal value: the logistic is off by less than that, act by |g| times it, y by |g u| times it
+    fp32 += np.abs(g * u) * 2.0 ** -126
     return y, fp32, fp32 + np.abs(y) * EPS16[dt] * (1 + 2.0 ** -8) + TINY16[dt] + 2.0 ** -126
 
 

@@ -25,8 +25,8 @@ from typing import Optional, Tuple
 import torch
 
 from . import (qlin_act_quant_fp8, qlin_act_quant_i8, qlin_gemv_fp8, qlin_gemv_fp8_blk, qlin_gemv_fp8_blk_ex,
-               qlin_gemv_fp8_w8a8, qlin_gemv_i8, qlin_gemv_w4, qlin_gemv_w4_bwd, qlin_glu_w4, qlin_glu_w4_bwd,
-               qlin_linear_i8, qlin_moe_ffn_mxfp4, qlin_moe_mxfp4)
+               qlin_gemv_fp8_w8a8, qlin_gemv_i8, qlin_gemv_w4, qlin_gemv_w4_bwd, qlin_glu_i8, qlin_glu_w4, qlin_glu_w4_bwd,
+               qlin_linear_i8, qlin_moe_ffn_i8, qlin_moe_ffn_mxfp4, qlin_moe_mxfp4)
 
 hits = collections.Counter()
 
@@ -73,6 +73,46 @@ def linear_i8(x: torch.Tensor, w: torch.Tensor, ws: torch.Tensor,
 @linear_i8.register_fake
 def _(x, w, ws, bias=None):
     return x.new_empty((x.shape[0], w.shape[0]), dtype=torch.bfloat16)
+
+
+@torch.library.custom_op("qlin::glu_i8", mutates_args=())
+def glu_i8(x: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor, act: int = 0) -> torch.Tensor:
+    """Gated feed-forward front on INT8 weights: dynamic per-token quantisation, both products, act(g) * u."""
+    hits["glu_i8"] += 1
+    return qlin_glu_i8(x, w13, s13, act=act)[0]
+
+
+@glu_i8.register_fake
+def _(x, w13, s13, act=0):
+    return x.new_empty((x.shape[0], w13.shape[0] // 2))
+
+
+@torch.library.custom_op("qlin::moe_ffn_i8", mutates_args=())
+def moe_ffn_i8(x: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor, w2: torch.Tensor, s2: torch.Tensor,
+               logits: torch.Tensor, topk: int, route: int = 0,
+               act: int = 0) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Mixture-of-experts layer on INT8 experts from the router's logits -> (y, ids, gw)."""
+    hits["moe_ffn_i8"] += 1
+    return qlin_moe_ffn_i8(x, w13, s13, w2, s2, logits=logits, topk=topk, route=route, act=act)
+
+
+@moe_ffn_i8.register_fake
+def _(x, w13, s13, w2, s2, logits, topk, route=0, act=0):
+    M = x.shape[0]
+    return (x.new_empty(x.shape), x.new_empty((M, topk), dtype=torch.int32), x.new_empty((M, topk), dtype=torch.float32))
+
+
+@torch.library.custom_op("qlin::moe_ffn_i8_given", mutates_args=())
+def moe_ffn_i8_given(x: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor, w2: torch.Tensor, s2: torch.Tensor,
+                     ids: torch.Tensor, gw: torch.Tensor, act: int = 0) -> torch.Tensor:
+    """The same layer with the experts and weights of each token given; an id outside the experts contributes nothing."""
+    hits["moe_ffn_i8_given"] += 1
+    return qlin_moe_ffn_i8(x, w13, s13, w2, s2, ids=ids, gw=gw, act=act)[0]
+
+
+@moe_ffn_i8_given.register_fake
+def _(x, w13, s13, w2, s2, ids, gw, act=0):
+    return x.new_empty(x.shape)
 
 
 # ----------------------------------------------------------------------------- FP8
