@@ -137,13 +137,13 @@ __global__ __launch_bounds__(256) void i8_combine_kernel(const float* part, cons
 }
 
 // columns [first, first + count) of the product with row_tiles tiles of BM rows (at most, where they are grouped)
-template <int T, int EPI, int BN, int BM, int WGN, int WGM>
+template <int T, int EPI, int BN, int BM, int WGN, int WGM, int D = 2>  // D: i8ffn_gemm.hpp
 hipError_t run_gemm(I8GemmParams p, int64_t row_tiles, int64_t first, int64_t count, hipStream_t st) {
     constexpr int CT = EPI == kI8Gated ? BN / 2 : BN;
     p.c_first = first;
     p.c_count = count;
     const int64_t tiles = row_tiles * ((count + CT - 1) / CT);
-    hipLaunchKernelGGL((i8_gemm_kernel<T, EPI, BN, BM, WGN, WGM>), dim3((unsigned)((tiles + 7) / 8 * 8)),
+    hipLaunchKernelGGL((i8_gemm_kernel<T, EPI, BN, BM, WGN, WGM, D>), dim3((unsigned)((tiles + 7) / 8 * 8)),
                        dim3(64 * WGN * WGM), 0, st, p);
     return hipGetLastError();
 }
@@ -232,13 +232,17 @@ hipError_t glu(const I8GluArgs& a, hipStream_t st) {
     g.x = a.xq; g.ldx = a.ldxq; g.xs = a.xs; g.R = a.M; g.div = 1;
     g.K = a.K; g.w = a.w13; g.ldw = a.ldw; g.N = 2 * a.I; g.ws = a.s13; g.ws_step = a.ws_step; g.C = a.I; g.act = a.act;
     g.y = a.y; g.ldy = a.ldy;
-    if (i8_dense_rows(a.M) == 64) return run_gemm<T, kI8Gated, 128, 64, 2, 2>(g, 1, 0, a.I, st);
-    const int64_t large = i8_large_columns(a.M, a.I);
+    const int64_t large = i8_large_columns(a.M, a.I), rest = a.I - large;
     if (large > 0) {
         const hipError_t l = run_gemm<T, kI8Gated, 256, 256, 4, 4>(g, (a.M + 255) / 256, 0, large, st);
-        if (l != hipSuccess || large == a.I) return l;
+        if (l != hipSuccess || rest == 0) return l;
     }
-    return run_gemm<T, kI8Gated, 128, 128, 2, 4>(g, (a.M + 127) / 128, large, a.I - large, st);
+    switch (i8_dense_tile(a.M, rest)) {
+        case kI8Tile64x64: return run_gemm<T, kI8Gated, 64, 64, 1, 2, 4>(g, (a.M + 63) / 64, large, rest, st);
+        case kI8Tile64x128: return run_gemm<T, kI8Gated, 128, 64, 2, 2, 4>(g, (a.M + 63) / 64, large, rest, st);
+        case kI8TwoOf128x128: return run_gemm<T, kI8Gated, 128, 128, 2, 4>(g, (a.M + 127) / 128, large, rest, st);
+        default: return run_gemm<T, kI8Gated, 128, 128, 2, 4, 4>(g, (a.M + 127) / 128, large, rest, st);
+    }
 }
 
 }  // namespace

@@ -6,11 +6,17 @@
 //
 // A workgroup owns BM code rows x BN weight rows and walks K 128 bytes at a
 // time.  Both tiles travel global -> LDS directly (global_load_lds_dwordx4, 8
-// rows x one whole 128-byte line an instruction) into two buffers; one barrier
-// a step.  The fragments of a 32-deep slice are read one slice ahead of their
-// products, and those of the next step's first slice right behind the barrier,
-// so a buffer is free for the loads of the step after next while the last
-// slice's products still run: a load has a whole step to arrive.
+// rows x one whole 128-byte line an instruction) into a ring of D buffers; one
+// barrier a step.  The fragments of a 32-deep slice are read one slice ahead of
+// their products, and those of the next step's first slice right behind the
+// barrier, so a buffer is free for the loads of D steps later while the last
+// slice's products still run: a load has D - 1 steps to arrive.
+//
+// D = 4 where a compute unit has one workgroup, as in a dense front of up to
+// some hundred tokens (2 x 4096 x 7168, cold: 509 tokens 63 -> 48 us, 256 61 ->
+// 44; 64 tokens in tiles of 64 rows 57 -> 36).  D = 2 where several share it
+// and hide each other's waits (1000 tokens, 64 experts top 6, 7168 x 2048: 729
+// us, 751 with 4), and in the 256 x 256 tile, whose two buffers fill LDS.
 #pragma once
 #include "i8ffn_device.hpp"
 
@@ -41,16 +47,18 @@ typedef int i32x4v_t __attribute__((ext_vector_type(4)));
 // Slot of 16-byte chunk c in LDS row r of 128 bytes: c ^ swz(r); see w4_gemm.hpp.
 __device__ __forceinline__ int i8_swz(int r) { return (r >> 1) & 7; }
 
+// This wave's loads into LDS but the last LATER are done, its reads too; then everyone's.
+template <int LATER>
 __device__ __forceinline__ void i8_stage_barrier() {
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    __builtin_amdgcn_s_waitcnt(0x70);  // vmcnt(0) lgkmcnt(0): this wave's loads into LDS are done, its reads too
+    __builtin_amdgcn_s_waitcnt((LATER & 15) | ((LATER >> 4) << 14) | 0x70);  // vmcnt(LATER) lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
 constexpr int kI8BandM = 8;  // row tiles per raster band
 
-template <int T, int EPI, int BN, int BM, int WGN, int WGM>
+template <int T, int EPI, int BN, int BM, int WGN, int WGM, int D>
 __global__ __launch_bounds__(64 * WGM * WGN, WGM * WGN == 16 ? 4 : 2) void i8_gemm_kernel(const I8GemmParams p) {
     constexpr int NW = WGM * WGN;
     constexpr int TM = BM / WGM / 32, TN = BN / WGN / 32;  // 32 x 32 tiles per wave
@@ -58,8 +66,11 @@ __global__ __launch_bounds__(64 * WGM * WGN, WGM * WGN == 16 ? 4 : 2) void i8_ge
     constexpr int XI = BM / 8 / NW, WI = BN / 8 / NW;      // 1 KB loads per wave and step
     constexpr int CT = EPI == kI8Gated ? BN / 2 : BN;      // output columns a tile
     static_assert(TM >= 1 && TN >= 1 && XI >= 1 && WI >= 1 && (EPI != kI8Gated || TN % 2 == 0), "tile");
+    static_assert(D == 2 || D == 4, "ring");
     // an object of its own for each tile: a load into one need not be waited for before another is read
     __shared__ __align__(16) uint8_t x_even[XT], x_odd[XT], w_even[WT], w_odd[WT];
+    __shared__ __align__(16) uint8_t x_third[D > 2 ? XT : 16], x_fourth[D > 2 ? XT : 16];
+    __shared__ __align__(16) uint8_t w_third[D > 2 ? WT : 16], w_fourth[D > 2 ? WT : 16];
     __shared__ int32_t rows[BM];  // the tile's output rows, their codes' scales: no load between the stores of the end
     __shared__ float scale[BM];
 
@@ -167,24 +178,41 @@ __global__ __launch_bounds__(64 * WGM * WGN, WGM * WGN == 16 ? 4 : 2) void i8_ge
                                                                   acc[i][j], 0, 0, 0);
     };
 
-    issue(0, x_even, w_even);
-    i8_stage_barrier();
-    load_frags(0, x_even, w_even, 0);
-    issue(nsteps > 1 ? 1 : 0, x_odd, w_odd);
     auto step = [&](int64_t s, uint8_t* xt, uint8_t* wt, uint8_t* xn, uint8_t* wnext) {
 #pragma unroll
         for (int ks = 0; ks < 3; ++ks) {
             load_frags((ks + 1) & 1, xt, wt, ks + 1);
             multiply(ks & 1);
         }
-        i8_stage_barrier();  // everyone's reads of step s are done, and the tiles of step s + 1 are there
+        i8_stage_barrier<(D - 2) * (XI + WI)>();  // everyone's reads of step s are done, and the tiles of step s + 1 are there
         load_frags(0, xn, wnext, 0);
-        issue(s + 2 < nsteps ? s + 2 : s, xt, wt);  // past the end: the idle tile, again
+        issue(s + D < nsteps ? s + D : s, xt, wt);  // past the end: the idle tile, again
         multiply(1);
     };
-    for (int64_t s = 0; s < nsteps; s += 2) {
-        step(s, x_even, w_even, x_odd, w_odd);
-        if (s + 1 < nsteps) step(s + 1, x_odd, w_odd, x_even, w_even);
+    issue(0, x_even, w_even);
+    issue(nsteps > 1 ? 1 : 0, x_odd, w_odd);
+    if constexpr (D > 2) {
+        issue(nsteps > 2 ? 2 : 0, x_third, w_third);
+        issue(nsteps > 3 ? 3 : 0, x_fourth, w_fourth);
+    }
+    i8_stage_barrier<(D - 1) * (XI + WI)>();
+    load_frags(0, x_even, w_even, 0);
+    int64_t s = 0;
+    if constexpr (D == 2) {
+        for (; s < nsteps; s += 2) {
+            step(s, x_even, w_even, x_odd, w_odd);
+            if (s + 1 < nsteps) step(s + 1, x_odd, w_odd, x_even, w_even);
+        }
+    } else {
+        for (; s + 4 <= nsteps; s += 4) {  // no branch inside: the compiler would wait for every load where two ways meet
+            step(s, x_even, w_even, x_odd, w_odd);
+            step(s + 1, x_odd, w_odd, x_third, w_third);
+            step(s + 2, x_third, w_third, x_fourth, w_fourth);
+            step(s + 3, x_fourth, w_fourth, x_even, w_even);
+        }
+        if (s < nsteps) step(s, x_even, w_even, x_odd, w_odd);
+        if (s + 1 < nsteps) step(s + 1, x_odd, w_odd, x_third, w_third);
+        if (s + 2 < nsteps) step(s + 2, x_third, w_third, x_fourth, w_fourth);
     }
     w4_wait_vmcnt<0>();  // no load into LDS outlives the workgroup
 

@@ -51,11 +51,23 @@ constexpr int64_t few_chunk(int64_t M, int64_t topk, int64_t E, int64_t I) {
 }
 
 // ---------------------------------------------------------------- more: i8ffn_gemm.hpp
-// Code rows of a tile.  Dense: 64 up to 64 tokens (128 tokens of 2 x 14336 x 4096: 45 us with either, 256: 83 and 52).
-// Experts: by what they have on average (64 experts, 7168 x 2048, front and down: 28 pairs each 345 + 216 us with
-// 64 rows, 372 + 258 with 128; 94 pairs each 509 + 349 and 409 + 303).
+// Code rows of an expert's tile, by what experts have on average (64 experts, 7168 x 2048, front and down: 28 pairs each
+// 345 + 216 us with 64 rows, 372 + 258 with 128; 94 pairs each 509 + 349 and 409 + 303).
 constexpr int i8_tile_rows(int64_t P, int64_t E) { return P <= 56 * E ? 64 : 128; }
-constexpr int i8_dense_rows(int64_t M) { return M <= 64 ? 64 : 128; }
+
+// Tile (code rows x weight rows) of a dense front: smaller ones where the larger leave half of the compute units idle.
+// 2 x 4096 x 7168: 64 tokens 29 us with 64 x 64, 36 with 64 x 128; 128 tokens 30, 36 and 44 with 128 x 128.
+// 2 x 14336 x 4096, 64 tokens: 36 us with 64 x 64, 34 with 64 x 128.  The rings of 128 x 128 are four deep, one workgroup
+// a compute unit; two deep where that lets all of them run at once (2 x 14336 x 4096: 200 tokens, 448 workgroups, 50 us
+// with two, 55 with four; 300 tokens, 672 workgroups, 82 and 76).
+enum I8DenseTile { kI8Tile64x64 = 0, kI8Tile64x128 = 1, kI8Tile128x128 = 2, kI8TwoOf128x128 = 3 };
+constexpr I8DenseTile i8_dense_tile(int64_t M, int64_t I) {
+    const int64_t columns = (I + 63) / 64;  // gated: 128 weight rows give 64 columns
+    const int64_t large = (M + 127) / 128 * columns;
+    if ((M + 63) / 64 * columns <= 128) return kI8Tile64x64;
+    if (M <= 64 || large <= 128) return kI8Tile64x128;
+    return large <= 256 || large > 512 ? kI8Tile128x128 : kI8TwoOf128x128;
+}
 
 // Output columns of a dense front that 256 x 256 tiles (128 columns) compute in whole rounds of 256.
 constexpr int64_t i8_large_columns(int64_t M, int64_t I) {

@@ -46,7 +46,7 @@ int main(int argc, char** argv) {
                       E = std::atoll(argv[6]);
         std::printf("%d %d %d %d %lld %lld %lld %lld %lld\n", few_fits(M, K), few_quantise(M, K), few_turn(K),
                     few_sets(M, topk, E), (long long)few_down_rows(M * topk, I), (long long)few_chunk(M, topk, E, I),
-                    (long long)(E > 0 ? i8_tile_rows(M * topk, E) : 0), (long long)i8_dense_rows(M),
+                    (long long)(E > 0 ? i8_tile_rows(M * topk, E) : 0), (long long)i8_dense_tile(M, I),
                     (long long)i8_large_columns(M, I));
         return 0;
     }

@@ -23,6 +23,13 @@ def test_glu_sizes(ql, M, I, K, dt):
     check_glu(ql, M, I, K, dt, seed=M + I)
 
 
+@pytest.mark.parametrize("K", [16, 128, 144, 384, 512, 640, 1040])
+@pytest.mark.parametrize("M,I", [(40, 8200), (70, 4100), (120, 8300), (130, 8200), (700, 5600), (1030, 6700)])
+def test_glu_tiles(ql, M, I, K):
+    """Widths that take every tile of the matrix kernel, with one to nine steps of K."""
+    check_glu(ql, M, I, K, "bf16" if K % 128 else "fp16", seed=K)
+
+
 @pytest.mark.parametrize("M", [1, 4, 16, 40])
 def test_glu_variants(ql, M):
     check_glu(ql, M, 50, 320, "bf16", kind=1, seed=1)

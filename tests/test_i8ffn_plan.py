@@ -6,7 +6,7 @@ import pytest
 
 from conftest import ROOT
 
-NAMES = ("fits", "quantise", "turn", "sets", "down_rows", "chunk", "tile_rows", "dense_rows", "large")
+NAMES = ("fits", "quantise", "turn", "sets", "down_rows", "chunk", "tile_rows", "dense_tile", "large")
 
 
 @pytest.fixture(scope="module")
@@ -38,7 +38,11 @@ def test_kernels_by_size(plan):
     assert [plan(1, K, 16)["turn"] for K in (16, 768, 1024, 1536, 2048, 2064, 4096, 5120, 7168, 14336)] == [
         3, 3, 4, 3, 4, 3, 4, 4, 4, 4]
     assert [plan(M, 7168, 2048, 6, 64)["tile_rows"] for M in (64, 300, 1000)] == [64, 64, 128]
-    assert [plan(M, 4096, 14336)["dense_rows"] for M in (17, 64, 65, 2048)] == [64, 64, 128, 128]
+    small, wide, square, two = range(4)  # 64 x 64, 64 x 128, 128 x 128 with a ring of four, of two
+    assert [plan(M, 4096, 14336)["dense_tile"] for M in (17, 64, 65, 128, 129, 256, 257)] == [
+        wide, wide, square, square, two, two, square]
+    assert [plan(M, 7168, 4096)["dense_tile"] for M in (17, 64, 128, 129, 256, 257)] == [
+        small, small, small, wide, wide, square]
     assert plan(1023, 4096, 14336)["large"] == 0 and plan(2048, 4096, 14336)["large"] == 96 * 128
 
 
