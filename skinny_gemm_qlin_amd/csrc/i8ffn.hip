@@ -168,7 +168,7 @@ MoeRegions regions(int64_t M, int64_t H, int64_t I, int64_t topk, int64_t E) {
     r.hq = take(P * I);
     r.hs = take(P * 4);
     r.part = take(P * H * 4);
-    r.tiles = take(most_tiles(P, E, 64) * (int64_t)sizeof(I8Tile));
+    r.tiles = take(most_tiles(P, E, 32) * (int64_t)sizeof(I8Tile));
     r.ntiles = take(4);
     r.perm = take(P * 4);
     r.list = take((int64_t)few_list_bytes());
@@ -207,15 +207,17 @@ hipError_t moe(const I8MoeArgs& a, hipStream_t st) {
     g.K = a.H; g.w = a.w13; g.ldw = a.ldw13; g.N = 2 * a.I; g.ws = a.s13; g.ws_step = 1; g.C = a.I; g.act = a.act;
     g.y = h; g.ldy = a.I;
     const int64_t most = most_tiles(P, a.E, bm);
-    e = bm == 64 ? run_gemm<T, kI8Gated, 128, 64, 2, 2>(g, most, 0, a.I, st)
-                 : run_gemm<T, kI8Gated, 128, 128, 2, 4>(g, most, 0, a.I, st);
+    e = bm == 32   ? run_gemm<T, kI8Gated, 128, 32, 2, 1>(g, most, 0, a.I, st)
+        : bm == 64 ? run_gemm<T, kI8Gated, 128, 64, 2, 2>(g, most, 0, a.I, st)
+                   : run_gemm<T, kI8Gated, 128, 128, 2, 4>(g, most, 0, a.I, st);
     if (e != hipSuccess) return e;
     e = quantise(T, h, a.I, P, a.I, hq, a.I, hs, a.ids, a.E, st);
     if (e != hipSuccess) return e;
     g.x = hq; g.ldx = a.I; g.xs = hs; g.div = 1; g.K = a.I; g.w = a.w2; g.ldw = a.ldw2; g.N = a.H; g.ws = a.s2;
     g.C = a.H; g.y = nullptr; g.part = part; g.ldy = a.H;
-    e = bm == 64 ? run_gemm<T, kI8Part, 128, 64, 4, 2>(g, most, 0, a.H, st)
-                 : run_gemm<T, kI8Part, 128, 128, 2, 4>(g, most, 0, a.H, st);
+    e = bm == 32   ? run_gemm<T, kI8Part, 128, 32, 4, 1>(g, most, 0, a.H, st)
+        : bm == 64 ? run_gemm<T, kI8Part, 128, 64, 4, 2>(g, most, 0, a.H, st)
+                   : run_gemm<T, kI8Part, 128, 128, 2, 4>(g, most, 0, a.H, st);
     if (e != hipSuccess) return e;
     const int64_t n = a.M * (a.H / 4);
     hipLaunchKernelGGL(i8_combine_kernel<T>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, part, a.ids, a.gw, a.M,

@@ -51,9 +51,10 @@ constexpr int64_t few_chunk(int64_t M, int64_t topk, int64_t E, int64_t I) {
 }
 
 // ---------------------------------------------------------------- more: i8ffn_gemm.hpp
-// Code rows of an expert's tile, by what experts have on average (64 experts, 7168 x 2048, front and down: 28 pairs each
-// 345 + 216 us with 64 rows, 372 + 258 with 128; 94 pairs each 509 + 349 and 409 + 303).
-constexpr int i8_tile_rows(int64_t P, int64_t E) { return P <= 56 * E ? 64 : 128; }
+// Code rows of an expert's tile, by what experts have on average.  64 experts, top 6, 7168 x 2048, calls: 17 tokens 368
+// us with 32 rows, 463 with 64; 150 tokens 527 and 536.  Front and down with 28 pairs each: 345 + 216 us with 64 rows,
+// 372 + 258 with 128; with 94 pairs each 509 + 349 and 409 + 303.
+constexpr int i8_tile_rows(int64_t P, int64_t E) { return P <= 16 * E ? 32 : (P <= 56 * E ? 64 : 128); }
 
 // Tile (code rows x weight rows) of a dense front: smaller ones where the larger leave half of the compute units idle.
 // 2 x 4096 x 7168: 64 tokens 29 us with 64 x 64, 36 with 64 x 128; 128 tokens 30, 36 and 44 with 128 x 128.

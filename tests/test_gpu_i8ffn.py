@@ -60,6 +60,14 @@ def test_moe_variants(ql, M):
     check_moe(ql, M, 5, 7, 80, 64, "fp16", kind=1, seed=M + 3, given=True)  # more slots than experts
 
 
+@pytest.mark.parametrize("K", [16, 128, 144, 384, 640])
+@pytest.mark.parametrize("M,E,topk", [(40, 8, 2), (90, 8, 2), (90, 2, 2)])
+def test_moe_tiles(ql, M, E, topk, K):
+    """Tiles of 32, 64 and 128 rows, with one to five steps of either reduction."""
+    check_moe(ql, M, E, topk, K, 208, "bf16", seed=K)
+    check_moe(ql, M, E, topk, 208, K, "fp16", seed=K)
+
+
 @pytest.mark.parametrize("M,E,topk,H,I", [(1, 2, 1, 40000, 32), (2, 2, 2, 48, 65536), (20, 2, 1, 40000, 32),
                                           (3, 1, 1, 131072, 16), (2, 2, 2, 16, 131072)])
 def test_moe_long_rows(ql, M, E, topk, H, I):

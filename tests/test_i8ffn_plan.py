@@ -37,7 +37,7 @@ def test_kernels_by_size(plan):
     assert [plan(M, 4096, 14336)["sets"] for M in (1, 4, 5, 8, 9, 16)] == [1, 1, 2, 2, 4, 4]
     assert [plan(1, K, 16)["turn"] for K in (16, 768, 1024, 1536, 2048, 2064, 4096, 5120, 7168, 14336)] == [
         3, 3, 4, 3, 4, 3, 4, 4, 4, 4]
-    assert [plan(M, 7168, 2048, 6, 64)["tile_rows"] for M in (64, 300, 1000)] == [64, 64, 128]
+    assert [plan(M, 7168, 2048, 6, 64)["tile_rows"] for M in (64, 171, 597, 598)] == [32, 64, 64, 128]
     small, wide, square, two = range(4)  # 64 x 64, 64 x 128, 128 x 128 with a ring of four, of two
     assert [plan(M, 4096, 14336)["dense_tile"] for M in (17, 64, 65, 128, 129, 256, 257)] == [
         wide, wide, square, square, two, two, square]
