@@ -43,8 +43,8 @@
  *   their quantisers) and qlin_moe_mxfp4 accept 1 <= M <= QLIN_MAX_M_PREFILL;
  *   up to 16 they run the decode kernels, above 16 a tiled (grouped, for
  *   the MoE) matrix-core GEMM with the same arithmetic contract.  The 4-bit
- *   weight calls accept the same range.  The routed
- *   expert FFN and the per-tensor FP8 quantiser take 1 <= M <= QLIN_MAX_M.
+ *   weight calls and the INT8 feed-forward calls accept the same range.  The
+ *   routed MXFP4 expert FFN and the per-tensor FP8 quantiser take 1 <= M <= QLIN_MAX_M.
  * - Base pointers and row pitches of weights, codes and bf16 activations must
  *   be 16-byte aligned (128-bit loads); scale arrays must be naturally
  *   aligned.
@@ -456,7 +456,8 @@ int qlin_glu_w4_bwd(const void* dy, int64_t lddy, int64_t M, int64_t I, int dtyp
  *   s = max_k |v[k]| / 127,  q = clamp(rne(v / s), -127, 127)
  * (IEEE fp32 quotients; an all-zero row has s = 0 and codes 0).  A row that
  * holds an infinity or a NaN has s = NaN and codes 0: the outputs that it feeds
- * are NaN, and no others.  dtype is the type of x and y.  K, H and I as
+ * are NaN, and no others.  dtype is the type of x and y.  No output overlaps an
+ * input or another output.  K, H and I as
  * reduction lengths are multiples of 16 in [16, 131072]; 1 <= M <=
  * QLIN_MAX_M_PREFILL; row pitches at most 2^30 elements. */
 
@@ -498,7 +499,7 @@ size_t qlin_moe_ffn_i8_workspace_bytes(int64_t M, int64_t H, int64_t I, int64_t 
  *   w13 int8 [E, 2I, ldw13] (gate rows, then up rows), s13 fp32 [E, 2I]
  *   w2  int8 [E, H, ldw2], s2 fp32 [E, H]
  *   ids int32 [M, topk], gw fp32 [M, topk] (outputs with logits, else inputs)
- *   y 16-bit [M, ldy]; overlaps no input
+ *   y 16-bit [M, ldy]
  *   workspace: 16-byte aligned, at least qlin_moe_ffn_i8_workspace_bytes();
  *      its contents on entry do not matter; calls that can overlap need one each.
  * 1 <= E <= 1024, 1 <= topk <= 16, with logits topk <= E.  Alignment: x, w13, w2

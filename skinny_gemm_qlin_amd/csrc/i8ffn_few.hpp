@@ -1,10 +1,19 @@
 // i8ffn_few.hpp -- the INT8 feed-forward operators for up to 16 tokens: kernels
 // that stream the live experts' weights (or the dense front's) once.
 //
-// Bound: the weights' bytes from HBM.  An item is a wave's own: 4 x RG weight
-// rows over the whole of K, so no wave waits for another and a wave's next item
-// is requested while its last one is multiplied.  The front's 4 rows are gate
-// and up of two outputs, the down projection's 4 adjacent outputs.
+// Bound: the weights' bytes from HBM.  An item is 4 weight rows over the whole of
+// K (front: gate and up of two outputs; down: 4 adjacent outputs).  A workgroup
+// of 8 waves a compute unit has a run of the items of all live experts, dealt to
+// its waves by turns of D x 256 K, so that every wave has as many as any other,
+// to one; an item on the border of two waves is joined in LDS in whole numbers.
+// A wave's loads run D steps ahead, across items, and are never drained: the
+// last turn of an item requests the first of the next.  16 waves a compute unit,
+// two workgroups, or items that are a wave's own were slower (one token, 2 x
+// 14336 x 4096: 25.5 us with whole items, 19.6 us now, 117 MB at 6.0 TB/s, where
+// a kernel that only loads them takes 18).  64 experts top 6, 7168 x 2048, front
+// and down: one token 31.9 + 19.8 us (5.5 and 4.5 TB/s), of which 6 and 5 go by
+// before the first product (routing, list, codes); 8 tokens 150 + 78 us (6.7 and
+// 6.6 TB/s).
 //
 // v_mfma_i32_4x4x4_16b_i8 multiplies 16 blocks of 4 rows x 4 columns, 4 K each.
 // A lane holds 4 K of row (or column) lane % 4 for block lane / 4, so with block
@@ -343,12 +352,13 @@ struct FewWork {
             at = c;
             const int here = i, t0 = t, end = turns - t < left ? turns : t + left;
             left -= end - t0;
-            if (left > 0 && ++i == per) {  // past the end: this item's rows, again
+            if (left > 0 && ++i == per) {
                 i = 0;
                 chunk = enter(++c);
             }
             t = 0;
-            const int8_t* next = row(i);
+            // past the end: a turn of the chunk's first rows, the same for every wave that ends in it, which the L2s hold
+            const int8_t* next = row(left > 0 ? i : 0);
             const f32x2v_t sc = scales(i);
             int sum[NS];
             few_item<NS, D>(ring, next, t0, end, K, cb, sum);
