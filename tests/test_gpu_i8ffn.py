@@ -47,7 +47,8 @@ def test_glu_long_rows(ql, M, I, K):
     (1, 1, 1, 16, 16), (1, 8, 2, 256, 64), (1, 64, 6, 512, 128), (2, 4, 4, 144, 48), (3, 128, 8, 272, 80),
     (5, 3, 2, 1040, 1040), (8, 64, 6, 512, 128), (13, 40, 5, 336, 112), (16, 16, 16, 128, 32), (16, 8, 2, 256, 512),
     (16, 1, 1, 512, 64), (17, 200, 8, 128, 64), (40, 8, 2, 256, 96), (64, 32, 4, 272, 96), (70, 1024, 8, 64, 32),
-    (200, 4, 2, 256, 128), (300, 16, 4, 144, 144)])
+    (200, 4, 2, 256, 128), (300, 16, 4, 144, 144), (1, 1024, 16, 64, 32), (16, 1024, 16, 48, 32), (5, 700, 16, 4096, 16),
+    (16, 130, 3, 528, 1040)])
 def test_moe_sizes(ql, M, E, topk, H, I, dt):
     check_moe(ql, M, E, topk, H, I, dt, seed=M + E)
 
