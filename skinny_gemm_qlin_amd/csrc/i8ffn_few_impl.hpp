@@ -59,11 +59,10 @@ hipError_t few_front(FewFrontParams& p, int8_t* xq, int64_t ldxq, float* xs, int
 
 template <int T, int SRC, int NS, int D>
 hipError_t run_down(FewDownParams& p, hipStream_t st) {
-    const int P = p.M * p.topk, groups = (int)(p.H / 4);
+    const int P = p.M * p.topk;
     p.rows = (int)few_down_rows(P, p.I);
-    const int grid = std::min(groups, kFewGrid), most = (groups + grid - 1) / grid;
-    p.block = std::max(1, std::min(most, kFewSums / (16 * P)));
-    hipLaunchKernelGGL((few_down_kernel<T, SRC, NS, D>), dim3((unsigned)grid), dim3(kFewThreads),
+    p.block = few_down_block(P, p.H);
+    hipLaunchKernelGGL((few_down_kernel<T, SRC, NS, D>), dim3((unsigned)few_down_grid(p.H)), dim3(kFewThreads),
                        (size_t)p.block * P * 16 + (size_t)p.rows * few_pitch(p.I, D), st, p);
     return hipGetLastError();
 }

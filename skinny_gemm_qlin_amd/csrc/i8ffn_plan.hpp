@@ -14,6 +14,7 @@ constexpr int kFewUnitsPerWave = 6, kFewUnits = kFewUnitsPerWave * kFewWaves;  /
 constexpr int kFewLds = 146 * 1024;  // dynamic LDS next to the lists, of 160 KB
 constexpr int kFewSums = 16 * 1024;  // of which the down projection's sums
 constexpr int kFewGrid = 256;        // compute units
+static_assert(kFewSums / (16 * kFewPairs) >= 1, "LDS holds the sums of a row group");
 
 // A turn: steps of 256 K that a wave's loads are ahead of its products.  An item's K is a whole number of turns, so
 // three where that saves steps (K = 768: 3 instead of 4; 2064: 9 instead of 12).
@@ -48,6 +49,15 @@ constexpr int64_t few_down_rows(int64_t P, int64_t I) {
 constexpr int64_t few_chunk(int64_t M, int64_t topk, int64_t E, int64_t I) {
     const int64_t n = few_down_rows(M * topk, I), s = 4 * few_sets(M, topk, E);
     return s < n ? s : n;
+}
+
+// Workgroups of the down projection, and the 4-row groups of the output whose sums one of them holds in LDS at once: a
+// workgroup whose share has more takes them in blocks of that many.
+constexpr int few_down_grid(int64_t H) { return H / 4 < kFewGrid ? (int)(H / 4) : kFewGrid; }
+constexpr int few_down_most(int64_t H) { return (int)((H / 4 + few_down_grid(H) - 1) / few_down_grid(H)); }
+constexpr int few_down_block(int64_t P, int64_t H) {
+    const int n = (int)(kFewSums / (16 * P));  // at least 4: P <= kFewPairs
+    return few_down_most(H) < n ? few_down_most(H) : n;
 }
 
 // ---------------------------------------------------------------- more: i8ffn_gemm.hpp
