@@ -16,8 +16,8 @@ from __future__ import annotations
 
 import torch
 
-from ._lib import (QLIN_ACT_GELU_TANH, QLIN_ACT_SILU, QLIN_DT_BF16, QLIN_DT_FP16, QLIN_FMT_E4M3,  # noqa: F401
-                   QLIN_FMT_E5M2, QLIN_ROUTE_ALL, QLIN_ROUTE_SELECTED, QlinError, check, load, status_str)
+from ._lib import (QLIN_ACT_GELU_TANH, QLIN_ACT_SILU, QLIN_DT_BF16, QLIN_DT_FP16, QLIN_ERR_SHAPE,  # noqa: F401
+                   QLIN_FMT_E4M3, QLIN_FMT_E5M2, QLIN_ROUTE_ALL, QLIN_ROUTE_SELECTED, QlinError, check, load, status_str)
 
 __all__ = [
     "QlinError", "qlin_act_quant_i8", "qlin_gemv_i8", "qlin_linear_i8", "qlin_gemv_fp8", "qlin_gemv_fp8_blk",
@@ -740,8 +740,12 @@ def qlin_moe_ffn_i8(x, w13, s13, w2, s2, logits=None, topk=None, route=QLIN_ROUT
     if not ok:
         _moe_i8_wrong(x, w13, s13, w2, s2, logits, topk, ids, gw, y, workspace)
     lib = load()
-    if workspace is None:
-        workspace = _own(None, (max(lib.qlin_moe_ffn_i8_workspace_bytes(M, H, I, topk, E), 1),), torch.uint8, x, stream)
+    if workspace is None or ids is None or gw is None:
+        need = lib.qlin_moe_ffn_i8_workspace_bytes(M, H, I, topk, E)
+        if need == 0:  # sizes that the call refuses: nothing is allocated for them
+            check(QLIN_ERR_SHAPE, "qlin_moe_ffn_i8")
+        if workspace is None:
+            workspace = _own(None, (need,), torch.uint8, x, stream)
     if ids is None:
         ids = _own(None, slots, torch.int32, x, stream)
     if gw is None:

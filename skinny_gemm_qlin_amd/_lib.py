@@ -39,6 +39,8 @@ QLIN_DT_FP16 = 1
 QLIN_ACT_SILU = 0
 QLIN_ACT_GELU_TANH = 1
 
+QLIN_ERR_SHAPE = -2
+
 QLIN_ROUTE_SELECTED = 0
 QLIN_ROUTE_ALL = 1
 
