@@ -467,8 +467,9 @@ int qlin_glu_w4_bwd(const void* dy, int64_t lddy, int64_t M, int64_t I, int dtyp
  *   y[m,i] = r16( act(g) * u )                           16-bit [M, ldy]
  *   x 16-bit [M, ldx]; s13 fp32 [2I] (ws_per_row = 1) or [1] (= 0)
  * The int32 sums are exact; act is QLIN_ACT_*.  1 <= I <= 2^20.  The down
- * projection is qlin_linear_i8 on y (bf16).  Alignment: x, w13, xq 16 bytes,
- * ldx % 8 == 0, ldw % 16 == 0, ldxq % 16 == 0. */
+ * projection is qlin_linear_i8 on y where y is bf16, which is all that it takes;
+ * an fp16 block as a whole is qlin_moe_ffn_i8 with one expert (ids 0, gw 1).
+ * Alignment: x, w13, xq 16 bytes, ldx % 8 == 0, ldw % 16 == 0, ldxq % 16 == 0. */
 int qlin_glu_i8(const void* x, int64_t ldx, int64_t M, int64_t K, int dtype,
                 const int8_t* w13, int64_t ldw, int64_t I, const float* s13, int ws_per_row, int act,
                 int8_t* xq, int64_t ldxq, float* xs, void* y, int64_t ldy, void* stream);

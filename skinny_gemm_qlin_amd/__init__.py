@@ -621,7 +621,8 @@ def qlin_glu_i8(x, w13, s13, act=QLIN_ACT_SILU, xq=None, xs=None, y=None, stream
     """Gated feed-forward front on INT8 weights: x bf16 or fp16 [M, K]; w13 int8
     [2I, K] (gate rows, then up rows; any row pitch that is a multiple of 16); s13
     fp32 [2I] or [1].  x is quantised per token (codes and scales into xq int8 [M, K]
-    / xs fp32 [M]).  Returns (y [M, I] of x's dtype, xq, xs)."""
+    / xs fp32 [M]).  Returns (y [M, I] of x's dtype, xq, xs).  The down projection of a
+    bf16 y is qlin_linear_i8; an fp16 block is qlin_moe_ffn_i8 with one expert."""
     try:
         dt, dtype, dev = _DT16.get(x.dtype), x.dtype, x.get_device()
         M, K = x.shape
