@@ -6,14 +6,15 @@
 // of 8 waves a compute unit has a run of the items of all live experts, dealt to
 // its waves by turns of D x 256 K, so that every wave has as many as any other,
 // to one; an item on the border of two waves is joined in LDS in whole numbers.
-// A wave's loads run D steps ahead, across items, and are never drained: the
-// last turn of an item requests the first of the next.  16 waves a compute unit,
-// two workgroups, or items that are a wave's own were slower (one token, 2 x
-// 14336 x 4096: 25.5 us with whole items, 19.6 us now, 117 MB at 6.0 TB/s, where
-// a kernel that only loads them takes 18).  64 experts top 6, 7168 x 2048, front
-// and down: one token 31.9 + 19.8 us (5.5 and 4.5 TB/s), of which 6 and 5 go by
-// before the first product (routing, list, codes); 8 tokens 150 + 78 us (6.7 and
-// 6.6 TB/s).
+// A wave's loads run D steps ahead, across items, and are not drained between
+// them: the last turn of an item requests the first of the next.  (They are where
+// the down projection goes on to another block of row groups or batch of codes.)
+// 16 waves a compute unit, two workgroups, or items that are a wave's own were
+// slower (one token, 2 x 14336 x 4096: 25.5 us with whole items, 19.5 us now, 117
+// MB at 6.0 TB/s, as a kernel that only loads them).  64 experts top 6, 7168 x
+// 2048, front and down: one token 31.9 + 19.9 us (5.5 and 4.4 TB/s; loads alone
+// 27.5 + 15.4), of which 6 and 5 go by before the first product (routing, list,
+// codes); 8 tokens 151 + 78 us (6.8 and 6.6 TB/s; loads alone 148 + 75).
 //
 // v_mfma_i32_4x4x4_16b_i8 multiplies 16 blocks of 4 rows x 4 columns, 4 K each.
 // A lane holds 4 K of row (or column) lane % 4 for block lane / 4, so with block
@@ -26,7 +27,9 @@
 //
 // Codes are in LDS: either each workgroup quantises the rows for itself while its
 // first weights travel (few rows: that costs less than a launch), or they were
-// written by a kernel ahead and are copied.
+// written by a kernel ahead and are copied.  The front's copy is not overlapped: the
+// tokens' scales and the list are loaded behind it, loads come back in order, and so
+// the first weights are requested when the codes have arrived.
 #pragma once
 #include <type_traits>
 

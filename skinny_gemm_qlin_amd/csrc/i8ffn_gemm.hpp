@@ -16,7 +16,9 @@
 // some hundred tokens (2 x 4096 x 7168, cold: 509 tokens 63 -> 48 us, 256 61 ->
 // 44; 64 tokens in tiles of 64 rows 57 -> 36).  D = 2 where several share it
 // and hide each other's waits (1000 tokens, 64 experts top 6, 7168 x 2048: 729
-// us, 751 with 4), and in the 256 x 256 tile, whose two buffers fill LDS.
+// us, 751 with 4), and in the 256 x 256 tile, whose two buffers fill LDS.  The
+// last D steps have nothing left to request and load their own slice again, which
+// the epilogue waits for: with D = 2 and K = 768 that is a quarter of the requests.
 #pragma once
 #include "i8ffn_device.hpp"
 
