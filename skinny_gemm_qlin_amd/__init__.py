@@ -740,13 +740,11 @@ def qlin_moe_ffn_i8(x, w13, s13, w2, s2, logits=None, topk=None, route=QLIN_ROUT
         ok = False
     if not ok:
         _moe_i8_wrong(x, w13, s13, w2, s2, logits, topk, ids, gw, y, workspace)
+    if logits is not None and not 0 < topk <= E:  # nothing is allocated for it
+        check(QLIN_ERR_SHAPE, "qlin_moe_ffn_i8")
     lib = load()
-    if workspace is None or ids is None or gw is None:
-        need = lib.qlin_moe_ffn_i8_workspace_bytes(M, H, I, topk, E)
-        if need == 0:  # sizes that the call refuses: nothing is allocated for them
-            check(QLIN_ERR_SHAPE, "qlin_moe_ffn_i8")
-        if workspace is None:
-            workspace = _own(None, (need,), torch.uint8, x, stream)
+    if workspace is None:
+        workspace = _own(None, (max(lib.qlin_moe_ffn_i8_workspace_bytes(M, H, I, topk, E), 1),), torch.uint8, x, stream)
     if ids is None:
         ids = _own(None, slots, torch.int32, x, stream)
     if gw is None:
